@@ -220,6 +220,81 @@ ivit_status ivit_layernorm_ptf(const int8_t *x, int64_t rows, int32_t cols, cons
                                ivit_dyadic out, int8_t *y, ivit_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * One shared model serving many requests: low-rank adapters, gated and scaled
+ * residual branches.  The pages have no counterpart; READING: each is put in the integer form of the operators above (int8
+ * tensors, dyadic requant with floor shifts, 32-bit accumulators).
+ * ------------------------------------------------------------------------- */
+
+/* n low-rank adapters of one linear layer [N x K], all of rank R (a multiple
+ * of 16, at most 128; a narrower adapter has zero rows of A).
+ *   A   [n x R x K] int8, down projections
+ *   b_t [n x R] int32 in [0, 2^31), c_t [n x R] int8 in [0, 31]: requant of
+ *       t = X A^T to int8, b_t / 2^c_t ~ S_x S_A / S_t
+ *   B   [n x N x R] int8, up projections, each entry at the scale
+ *       S_x S_w[j] / S_t[r], so that t B^T joins the layer's accumulator as
+ *       it is (|t B^T| <= 2^14 R accumulator units).                         */
+typedef struct {
+  int32_t n, R;
+  const int8_t *A;
+  const int32_t *b_t;
+  const int8_t *c_t;
+  const int8_t *B;
+} ivit_lora;
+
+/* Bytes of device workspace ivit_linear_lora needs (t of every row).        */
+size_t ivit_linear_lora_workspace_bytes(int64_t M, int32_t R);
+
+/* The linear layer of ivit_linear_requant with an adapter chosen per request:
+ * request q is the rows [q * rows, (q + 1) * rows) of X (the tokens of one
+ * image; rows = 1: every row its own), a = idx[q] its adapter, and
+ *   t_ir   = sat_8((b_t[a,r] * sum_k X[i,k] * A[a,r,k]) >> c_t[a,r])
+ *   acc_ij = sum_k X[i,k] * W[j,k] + bias[j] + sum_r t_ir * B[a,j,r]
+ * with everything after acc as in ivit_linear_requant.  An idx outside
+ * [0, lora->n) selects no adapter: the last sum is absent.  rounding applies
+ * to both requants.
+ * idx [M / rows] int32 (device); M a multiple of rows >= 1; workspace:
+ * ivit_linear_lora_workspace_bytes(M, R) bytes, 256-byte aligned, not used
+ * concurrently by another call.  Other constraints as ivit_linear_requant.  */
+ivit_status ivit_linear_lora(const int8_t *X, int64_t M, int32_t K, const int8_t *W, int32_t N, const int32_t *bias,
+                             const int32_t *b, const int8_t *c, int32_t out_bits, int32_t rounding,
+                             const ivit_lora *lora, const int32_t *idx, int64_t rows, const int8_t *skip,
+                             ivit_residual res, int8_t *Y, void *workspace, size_t workspace_bytes,
+                             ivit_stream_t stream);
+
+/* ivit_linear_shiftgelu with an adapter per request, as ivit_linear_lora.   */
+ivit_status ivit_linear_lora_shiftgelu(const int8_t *X, int64_t M, int32_t K, const int8_t *W, int32_t N,
+                                       const int32_t *bias, const int32_t *b, const int8_t *c, int32_t rounding,
+                                       const ivit_lora *lora, const int32_t *idx, int64_t rows, int32_t gelu_I0,
+                                       int32_t gelu_M, int32_t gelu_k_out, ivit_dyadic gelu_out, int8_t *Y,
+                                       void *workspace, size_t workspace_bytes, ivit_stream_t stream);
+
+/* Parameters of one I-LayerNorm, as ivit_layernorm takes them.              */
+typedef struct {
+  const int8_t *gamma;
+  const int32_t *beta;
+  int32_t F, M_ln;
+  ivit_dyadic out;
+} ivit_norm;
+
+/* The end of a residual branch in one pass: the norm after the branch, its
+ * gate, its residual scale, the residual sum, the norm before the next branch.
+ *   n_ij = post ? I-LayerNorm_post(branch)_ij : branch_ij      (ivit_layernorm)
+ *   u_ij = gate ? n_ij * gate[i / gate_rows, j] : n_ij
+ *   y_ij = sat_8((b_skip * skip_ij + scale_j * u_ij) >> c)
+ *   z_ij = I-LayerNorm_pre(y)_ij                                (pre not NULL)
+ * skip, branch, y, z [rows x cols] int8 (z unused without pre).  y and z may
+ * each be skip or branch itself (in place); any other overlap of an output
+ * with another tensor of the call is IVIT_ERR_INVALID_ARG.  gate [ceil(rows / gate_rows) x cols] int8, one row per
+ * request of gate_rows rows; scale [cols] int32, any sign: LayerScale's
+ * lambda_j S_n (S_gate) / S_y over the common shift c; b_skip / 2^c ~
+ * S_skip / S_y.  Constraints: rows >= 0; cols and both norms' F, M_ln and out
+ * as ivit_layernorm; b_skip >= 0; 0 <= c <= 31; gate_rows >= 1.             */
+ivit_status ivit_residual_norm(const int8_t *skip, const int8_t *branch, int64_t rows, int32_t cols,
+                               const ivit_norm *post, const int8_t *gate, int64_t gate_rows, const int32_t *scale,
+                               int32_t b_skip, int32_t c, const ivit_norm *pre, int8_t *y, int8_t *z,
+                               ivit_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * The encoder block ([IVIT] 3.1): X^ = MSA(LN1(X)) + X; Y = MLP(LN2(X^)) + X^
  * ------------------------------------------------------------------------- */
 

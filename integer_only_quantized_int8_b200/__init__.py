@@ -25,6 +25,8 @@ __all__ = [
     "ModelParams", "ivit_patch_embed_workspace_bytes", "ivit_patch_embed", "ivit_head_workspace_bytes", "ivit_head",
     "ivit_model_workspace_bytes", "ivit_model_forward", "ivit_selftest_wait_timeout", "ivit_selftest_int_rate",
     "ivit_shiftgelu_rowmax", "ivit_attention_lis", "ivit_layernorm_ptf", "ivit_selftest_withhold",
+    "Lora", "Norm", "ivit_linear_lora_workspace_bytes", "ivit_linear_lora", "ivit_linear_lora_shiftgelu",
+    "ivit_residual_norm",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +44,7 @@ EXPORTED_SYMBOLS = (
     "ivit_model_workspace_bytes", "ivit_model_forward",
     "ivit_selftest_wait_timeout", "ivit_selftest_int_rate",
     "ivit_shiftgelu_rowmax", "ivit_attention_lis", "ivit_layernorm_ptf", "ivit_selftest_withhold",
+    "ivit_linear_lora_workspace_bytes", "ivit_linear_lora", "ivit_linear_lora_shiftgelu", "ivit_residual_norm",
 )
 
 _STATUS = {0: "IVIT_OK", 1: "IVIT_ERR_INVALID_ARG", 2: "IVIT_ERR_UNSUPPORTED", 3: "IVIT_ERR_CUDA",
@@ -60,6 +63,17 @@ class Dyadic(C.Structure):
 
 class Residual(C.Structure):
     _fields_ = [("b_skip", C.c_int32), ("b_branch", C.c_int32), ("c", C.c_int32)]
+
+
+class Lora(C.Structure):
+    """Mirror of ``ivit_lora``."""
+    _fields_ = [("n", C.c_int32), ("R", C.c_int32), ("A", C.c_void_p), ("b_t", C.c_void_p), ("c_t", C.c_void_p),
+                ("B", C.c_void_p)]
+
+
+class Norm(C.Structure):
+    """Mirror of ``ivit_norm``."""
+    _fields_ = [("gamma", C.c_void_p), ("beta", C.c_void_p), ("F", C.c_int32), ("M_ln", C.c_int32), ("out", Dyadic)]
 
 
 class BlockParams(C.Structure):
@@ -157,6 +171,17 @@ def lib() -> C.CDLL:
             L.ivit_attention_lis.argtypes = [vp, i32, i32, i32, Dyadic, i32, i32, i32, Dyadic, vp, vp]
             L.ivit_layernorm_ptf.restype = C.c_int
             L.ivit_layernorm_ptf.argtypes = [vp, i64, i32, vp, vp, vp, i32, i32, Dyadic, vp, vp]
+            L.ivit_linear_lora_workspace_bytes.restype = C.c_size_t
+            L.ivit_linear_lora_workspace_bytes.argtypes = [i64, i32]
+            L.ivit_linear_lora.restype = C.c_int
+            L.ivit_linear_lora.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, i32, i32, C.POINTER(Lora), vp, i64, vp,
+                                           Residual, vp, vp, C.c_size_t, vp]
+            L.ivit_linear_lora_shiftgelu.restype = C.c_int
+            L.ivit_linear_lora_shiftgelu.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, i32, C.POINTER(Lora), vp, i64,
+                                                     i32, i32, i32, Dyadic, vp, vp, C.c_size_t, vp]
+            L.ivit_residual_norm.restype = C.c_int
+            L.ivit_residual_norm.argtypes = [vp, vp, i64, i32, C.POINTER(Norm), vp, i64, vp, i32, i32,
+                                             C.POINTER(Norm), vp, vp, vp]
             L.ivit_selftest_withhold.restype = C.c_int
             L.ivit_selftest_withhold.argtypes = [i32, i32]
             L.ivit_selftest_int_rate.restype = C.c_int
@@ -198,6 +223,15 @@ def _holds(n: int, **tensors):
     for name, t in tensors.items():
         if t is not None and t.numel() < n:
             raise ValueError(f"{name} holds {t.numel()} elements, needs {n}")
+
+
+def _here(t, dtype, name):
+    """_ptr of a tensor that must also live on the current device, where the
+    call's kernels and (without an explicit one) its stream are."""
+    p = _ptr(t, dtype, name)
+    if t is not None and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return p
 
 
 def _dy(d) -> Dyadic:
@@ -336,6 +370,94 @@ def ivit_layernorm_ptf(x, alpha, gamma, beta, F: int, M_ln: int, out, y, stream=
                                   int(M_ln), _dy(out), _ptr(y, torch.int8, "y"), _stream(stream))
     _check("ivit_layernorm_ptf", st)
     return y
+
+
+def ivit_linear_lora_workspace_bytes(M: int, R: int) -> int:
+    return int(lib().ivit_linear_lora_workspace_bytes(int(M), int(R)))
+
+
+def _lora_args(X, W, bias, b, c, adapters, idx, rows, Y, skip=None):
+    """Shape checks shared by the linear layers with adapters; (M, K, N, Lora, idx pointer)."""
+    M, K = X.shape
+    N = W.shape[0]
+    A, b_t, c_t, B = adapters
+    n, R = A.shape[0], A.shape[1]
+    if W.shape[1] != K or tuple(Y.shape) != (M, N) or tuple(A.shape) != (n, R, K) or tuple(B.shape) != (n, N, R):
+        raise ValueError("shape mismatch")
+    if skip is not None and tuple(skip.shape) != (M, N):
+        raise ValueError("skip shape mismatch")
+    if rows < 1 or M % rows:
+        raise ValueError(f"shape mismatch: {M} rows are not requests of {rows}")
+    _holds(N, bias=bias, b=b, c=c)
+    _holds(n * R, b_t=b_t, c_t=c_t)
+    _holds(M // rows, idx=idx)
+    lora = Lora(n, R, _here(A, torch.int8, "A"), _here(b_t, torch.int32, "b_t"), _here(c_t, torch.int8, "c_t"),
+                _here(B, torch.int8, "B"))
+    return M, K, N, lora, _here(idx, torch.int32, "idx")
+
+
+def ivit_linear_lora(X, W, bias, b, c, adapters, idx, rows: int, Y, workspace, out_bits: int = 8, skip=None, res=None,
+                     stream=None, rounding: int = 0):
+    """ivit_linear_requant with a low-rank adapter per request: rows [q * rows, (q + 1) * rows) of X take adapter
+    idx[q] of ``adapters`` = (A [n,R,K] int8, b_t [n,R] int32, c_t [n,R] int8, B [n,N,R] int8), or none where idx[q]
+    is outside [0, n)."""
+    M, K, N, lora, pidx = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y, skip)
+    st = lib().ivit_linear_lora(_here(X, torch.int8, "X"), M, K, _here(W, torch.int8, "W"), N,
+                                _here(bias, torch.int32, "bias"), _here(b, torch.int32, "b"), _here(c, torch.int8, "c"),
+                                int(out_bits), int(rounding), C.byref(lora), pidx, int(rows),
+                                _here(skip, torch.int8, "skip"), _res(res), _here(Y, torch.int8, "Y"),
+                                _here(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
+    _check("ivit_linear_lora", st)
+    return Y
+
+
+def ivit_linear_lora_shiftgelu(X, W, bias, b, c, adapters, idx, rows: int, gelu_I0: int, gelu_M: int, gelu_k_out: int,
+                               gelu_out, Y, workspace, stream=None, rounding: int = 0):
+    """ivit_linear_shiftgelu with an adapter per request, as ivit_linear_lora."""
+    M, K, N, lora, pidx = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y)
+    st = lib().ivit_linear_lora_shiftgelu(_here(X, torch.int8, "X"), M, K, _here(W, torch.int8, "W"), N,
+                                          _here(bias, torch.int32, "bias"), _here(b, torch.int32, "b"),
+                                          _here(c, torch.int8, "c"), int(rounding), C.byref(lora), pidx, int(rows),
+                                          int(gelu_I0), int(gelu_M), int(gelu_k_out), _dy(gelu_out),
+                                          _here(Y, torch.int8, "Y"), _here(workspace, torch.uint8, "workspace"),
+                                          workspace.numel(), _stream(stream))
+    _check("ivit_linear_lora_shiftgelu", st)
+    return Y
+
+
+def _norm(n, name):
+    """A ctypes Norm from (gamma, beta, F, M_ln, out), or None."""
+    if n is None:
+        return None
+    gamma, beta, F, M_ln, out = n
+    return C.byref(Norm(_here(gamma, torch.int8, f"{name} gamma"), _here(beta, torch.int32, f"{name} beta"), int(F),
+                        int(M_ln), _dy(out)))
+
+
+def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, gate=None, gate_rows: int = 1, pre=None,
+                       z=None, stream=None):
+    """The end of a residual branch in one pass: y = sat_8((b_skip skip + scale_j u) >> c) with u the branch, after
+    its I-LayerNorm ``post`` and times its request's row of ``gate``, and z = I-LayerNorm ``pre`` of y.  skip, branch,
+    y, z [rows, cols] int8; post and pre (gamma, beta, F, M_ln, out) or None; gate [ceil(rows / gate_rows), cols] int8
+    or None; scale [cols] int32.  Returns (y, z)."""
+    rows, cols = skip.shape
+    if tuple(branch.shape) != (rows, cols) or tuple(y.shape) != (rows, cols) or scale.numel() != cols:
+        raise ValueError("shape mismatch")
+    if (pre is None) != (z is None) or (z is not None and tuple(z.shape) != (rows, cols)):
+        raise ValueError("z shape mismatch: z goes with pre")
+    if gate is not None:
+        if gate_rows < 1:
+            raise ValueError("shape mismatch: gate_rows < 1")
+        _holds(-(-rows // gate_rows) * cols, gate=gate)
+    for name, n in (("post", post), ("pre", pre)):
+        if n is not None and (n[0].numel() != cols or n[1].numel() != cols):
+            raise ValueError(f"{name} shape mismatch")
+    st = lib().ivit_residual_norm(_here(skip, torch.int8, "skip"), _here(branch, torch.int8, "branch"), rows, cols,
+                                  _norm(post, "post"), _here(gate, torch.int8, "gate"), int(gate_rows),
+                                  _here(scale, torch.int32, "scale"), int(b_skip), int(c), _norm(pre, "pre"),
+                                  _here(y, torch.int8, "y"), _here(z, torch.int8, "z"), _stream(stream))
+    _check("ivit_residual_norm", st)
+    return y, z
 
 
 def ivit_block_workspace_bytes(B: int, N: int, D: int, Dm: int) -> int:

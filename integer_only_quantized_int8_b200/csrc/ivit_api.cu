@@ -61,9 +61,9 @@ ivit_status device_ctx(DeviceCtx* out) {
   return IVIT_OK;
 }
 
-ivit_status encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                              uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
-                              CUtensorMapSwizzle swizzle) {
+namespace {
+// The driver's tensor-map encoder, looked up once; nullptr without a driver.
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -71,14 +71,36 @@ ivit_status encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
-  if (!g_encode) return IVIT_ERR_CUDA;
+  return g_encode;
+}
+}  // namespace
+
+ivit_status encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                              uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
+                              CUtensorMapSwizzle swizzle) {
+  const auto encode = tmap_encoder();
+  if (!encode) return IVIT_ERR_CUDA;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {row_stride_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? IVIT_OK : IVIT_ERR_CUDA;
+}
+
+ivit_status encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                              uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle) {
+  const auto encode = tmap_encoder();
+  if (!encode) return IVIT_ERR_CUDA;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {d0, d0 * d1};
+  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? IVIT_OK : IVIT_ERR_CUDA;
 }
 
@@ -94,6 +116,21 @@ bool valid_residual(ivit_residual r) {
 }
 bool valid_shiftmax(int32_t I0, int32_t M, int32_t k_out) {
   return I0 >= 1 && I0 <= (1 << 22) && k_out >= 1 && k_out <= 8 && M >= k_out - 1 && M <= 30;
+}
+
+// The host-side checks of one linear layer.
+ivit_status check_linear(const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N, const int32_t* bias,
+                         const int32_t* b, const int8_t* c, int32_t out_bits, int32_t rounding, const int8_t* skip,
+                         ivit_residual res, const int8_t* Y) {
+  if (!X || !W || !b || !c || !Y || (rounding != 0 && rounding != 1)) return IVIT_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(b) || !aligned16(c) || !aligned16(Y) ||
+      (bias && !aligned16(bias)) || (skip && !aligned16(skip)))
+    return IVIT_ERR_INVALID_ARG;
+  if (M < 1 || K < 16 || K % 16 != 0 || N < 16 || N % 16 != 0 || out_bits < 2 || out_bits > 8)
+    return IVIT_ERR_INVALID_ARG;
+  if (K > 16384 || M > 0x7fffff00LL) return IVIT_ERR_UNSUPPORTED;
+  if (skip && !valid_residual(res)) return IVIT_ERR_INVALID_ARG;
+  return IVIT_OK;
 }
 
 ivit_status dyadic_impl(double s, int32_t* b, int32_t* c) {
@@ -168,16 +205,10 @@ ivit_status ivit_linear_requant(const int8_t* X, int64_t M, int32_t K, const int
                                 const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits,
                                 int32_t rounding, const int8_t* skip, ivit_residual res, int8_t* Y,
                                 ivit_stream_t stream) {
-  if (!X || !W || !b || !c || !Y || (rounding != 0 && rounding != 1)) return IVIT_ERR_INVALID_ARG;
-  if (!aligned16(X) || !aligned16(W) || !aligned16(b) || !aligned16(c) || !aligned16(Y) ||
-      (bias && !aligned16(bias)) || (skip && !aligned16(skip)))
-    return IVIT_ERR_INVALID_ARG;
-  if (M < 1 || K < 16 || K % 16 != 0 || N < 16 || N % 16 != 0 || out_bits < 2 || out_bits > 8)
-    return IVIT_ERR_INVALID_ARG;
-  if (K > 16384 || M > 0x7fffff00LL) return IVIT_ERR_UNSUPPORTED;
-  if (skip && !valid_residual(res)) return IVIT_ERR_INVALID_ARG;
+  ivit_status st = check_linear(X, M, K, W, N, bias, b, c, out_bits, rounding, skip, res, Y);
+  if (st != IVIT_OK) return st;
   DeviceCtx dc;
-  ivit_status st = device_ctx(&dc);
+  st = device_ctx(&dc);
   if (st != IVIT_OK) return st;
   return launch_gemm(dc, X, M, K, W, N, bias, b, c, out_bits, rounding != 0, skip ? kEpiResidual : kEpiPlain, skip,
                      res, nullptr, Y,
@@ -289,6 +320,114 @@ ivit_status ivit_layernorm_ptf(const int8_t* x, int64_t rows, int32_t cols, cons
   ivit_status st = device_ctx(&dc);
   if (st != IVIT_OK) return st;
   return launch_layernorm_ptf(dc, x, rows, cols, alpha, gamma, beta, F, M_ln, out, y, (cudaStream_t)stream);
+}
+
+size_t ivit_linear_lora_workspace_bytes(int64_t M, int32_t R) {
+  if (M < 0 || R < 0) return 0;
+  return ((size_t)M * (size_t)R + 255) / 256 * 256;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks that ivit_linear_lora adds to those of the layer itself.
+ivit_status check_lora(const ivit_lora* l, const int32_t* idx, int64_t rows, int64_t M, const void* workspace,
+                       size_t workspace_bytes) {
+  if (!l || !idx || !workspace || !l->A || !l->b_t || !l->c_t || !l->B) return IVIT_ERR_INVALID_ARG;
+  if (!aligned16(idx) || !aligned16(l->A) || !aligned16(l->b_t) || !aligned16(l->c_t) || !aligned16(l->B) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return IVIT_ERR_INVALID_ARG;
+  if (l->n < 1 || l->R < 16 || l->R > 128 || l->R % 16 != 0 || rows < 1 || M % rows != 0) return IVIT_ERR_INVALID_ARG;
+  if (workspace_bytes < ivit_linear_lora_workspace_bytes(M, l->R)) return IVIT_ERR_INVALID_ARG;
+  return IVIT_OK;
+}
+
+// A checked linear layer with adapters: the down projection, then the GEMM
+// that takes the up projection along.
+ivit_status enqueue_lora(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
+                         const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits, bool round,
+                         const ivit_lora* l, const int32_t* idx, int64_t rows, EpiMode mode, const int8_t* skip,
+                         ivit_residual res, const GeluParams* gelu, int8_t* Y, void* workspace, cudaStream_t s) {
+  int8_t* T = static_cast<int8_t*>(workspace);
+  const LoraGemm lg{T, l->B, idx, l->n, l->R, rows};
+  const ivit_status st = launch_lora_down(dc, X, M, K, l->A, l->b_t, l->c_t, round, lg, T, s);
+  if (st != IVIT_OK) return st;
+  return launch_gemm(dc, X, M, K, W, N, bias, b, c, out_bits, round, mode, skip, res, gelu, Y, s, &lg);
+}
+
+// Whether the n bytes at a and the m bytes at b share any.
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uint64_t)m && y < x + (uint64_t)n;
+}
+
+bool valid_norm(const ivit_norm* n) {
+  return n->gamma && n->beta && aligned16(n->gamma) && aligned16(n->beta) && n->F >= 0 && n->F <= 14 &&
+         n->M_ln >= n->F && n->M_ln <= 23 && valid_dyadic(n->out);
+}
+
+}  // namespace
+
+extern "C" {
+
+ivit_status ivit_linear_lora(const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N, const int32_t* bias,
+                             const int32_t* b, const int8_t* c, int32_t out_bits, int32_t rounding,
+                             const ivit_lora* lora, const int32_t* idx, int64_t rows, const int8_t* skip,
+                             ivit_residual res, int8_t* Y, void* workspace, size_t workspace_bytes,
+                             ivit_stream_t stream) {
+  ivit_status st = check_linear(X, M, K, W, N, bias, b, c, out_bits, rounding, skip, res, Y);
+  if (st != IVIT_OK) return st;
+  if ((st = check_lora(lora, idx, rows, M, workspace, workspace_bytes)) != IVIT_OK) return st;
+  DeviceCtx dc;
+  if ((st = device_ctx(&dc)) != IVIT_OK) return st;
+  return enqueue_lora(dc, X, M, K, W, N, bias, b, c, out_bits, rounding != 0, lora, idx, rows,
+                      skip ? kEpiResidual : kEpiPlain, skip, res, nullptr, Y, workspace, (cudaStream_t)stream);
+}
+
+ivit_status ivit_linear_lora_shiftgelu(const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
+                                       const int32_t* bias, const int32_t* b, const int8_t* c, int32_t rounding,
+                                       const ivit_lora* lora, const int32_t* idx, int64_t rows, int32_t gelu_I0,
+                                       int32_t gelu_M, int32_t gelu_k_out, ivit_dyadic gelu_out, int8_t* Y,
+                                       void* workspace, size_t workspace_bytes, ivit_stream_t stream) {
+  if (!valid_shiftmax(gelu_I0, gelu_M, gelu_k_out) || !valid_dyadic(gelu_out)) return IVIT_ERR_INVALID_ARG;
+  const ivit_residual none{0, 0, 0};
+  ivit_status st = check_linear(X, M, K, W, N, bias, b, c, 8, rounding, nullptr, none, Y);
+  if (st != IVIT_OK) return st;
+  if ((st = check_lora(lora, idx, rows, M, workspace, workspace_bytes)) != IVIT_OK) return st;
+  DeviceCtx dc;
+  if ((st = device_ctx(&dc)) != IVIT_OK) return st;
+  const GeluParams gp{gelu_I0, gelu_M, gelu_k_out, gelu_out};
+  return enqueue_lora(dc, X, M, K, W, N, bias, b, c, 8, rounding != 0, lora, idx, rows, kEpiGelu, nullptr, none, &gp,
+                      Y, workspace, (cudaStream_t)stream);
+}
+
+ivit_status ivit_residual_norm(const int8_t* skip, const int8_t* branch, int64_t rows, int32_t cols,
+                               const ivit_norm* post, const int8_t* gate, int64_t gate_rows, const int32_t* scale,
+                               int32_t b_skip, int32_t c, const ivit_norm* pre, int8_t* y, int8_t* z,
+                               ivit_stream_t stream) {
+  if (rows < 0 || cols < 16 || cols > 2048 || cols % 16 != 0 || b_skip < 0 || c < 0 || c > 31 ||
+      (gate && gate_rows < 1))
+    return IVIT_ERR_INVALID_ARG;
+  if ((post && !valid_norm(post)) || (pre && !valid_norm(pre))) return IVIT_ERR_INVALID_ARG;
+  if (rows == 0) return IVIT_OK;
+  if (!skip || !branch || !scale || !y || (pre && !z) || !aligned16(skip) || !aligned16(branch) || !aligned16(scale) ||
+      !aligned16(y) || (gate && !aligned16(gate)) || (pre && !aligned16(z)))
+    return IVIT_ERR_INVALID_ARG;
+  // a thread writes y and z only where it has read skip and branch before, so an
+  // output in an input's exact place is fine; any other overlap is not
+  const int64_t n = rows * cols;
+  for (const int8_t* out : {y, pre ? z : y}) {
+    if ((out != skip && overlap(out, n, skip, n)) || (out != branch && overlap(out, n, branch, n)) ||
+        (gate && overlap(out, n, gate, ((rows - 1) / gate_rows + 1) * cols)))
+      return IVIT_ERR_INVALID_ARG;
+  }
+  if (pre && overlap(y, n, z, n)) return IVIT_ERR_INVALID_ARG;
+  DeviceCtx dc;
+  const ivit_status st = device_ctx(&dc);
+  if (st != IVIT_OK) return st;
+  return launch_residual_norm(dc, skip, branch, rows, cols, post, gate, gate_rows, scale, b_skip, c, pre, y, z,
+                              (cudaStream_t)stream);
 }
 
 size_t ivit_block_workspace_bytes(int32_t B, int32_t N, int32_t D, int32_t Dm) {

@@ -139,6 +139,15 @@ IVIT_DEV void tma_load_2d(void* smem_dst, const CUtensorMap* map, int32_t x, int
       : "memory");
 }
 
+// box of a 3D tensor map; parts of the box outside the map read as zeros
+IVIT_DEV void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // shared -> global tile store, tracked in the issuing thread's bulk groups
 IVIT_DEV void tma_store_2d(const CUtensorMap* map, int32_t x, int32_t y, const void* smem_src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(

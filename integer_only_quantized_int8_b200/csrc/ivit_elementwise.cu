@@ -468,7 +468,280 @@ __global__ void __launch_bounds__(kPtfThreads)
   }
 }
 
+// ---------------------------------------------------------------------------
+// The end of a branch in one pass (ivit_residual_norm): the norm after the
+// branch, the per-request gate, the residual scale, the sum with the skip
+// tensor, and the norm before the next branch.  A row is read once, stays in
+// registers between its two norms and is written once per output: half the
+// bytes of the separate operators.  kLnLanes lanes share a row as in
+// layernorm_staged_kernel; the per-channel tables are staged in shared memory
+// by each CTA, which then walks rows.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const int8_t* gamma;
+  const int32_t* beta;
+  int32_t F, M_ln;
+  ivit_dyadic out;
+  int32_t out_bq;  // b 2^(32 - c) when that fits a positive int32 (the requant is one mul.hi), else 0
+  int32_t fast;    // the mul.hi form applies
+};
+
+struct ResNormArgs {
+  const int8_t* skip;
+  const int8_t* branch;
+  int64_t rows;
+  int32_t cols;
+  NormArgs post, pre;
+  const int8_t* gate;
+  int64_t gate_rows;
+  const int32_t* scale;
+  int32_t b_skip, c;
+  int32_t fast_res;  // every shifted residual sum fits int32
+  int8_t* y;
+  int8_t* z;
+};
+
+// (x - mu) f of one row from its sums: f = floor(2^M_ln / sigma), muf = mu f
+__device__ __forceinline__ void norm_row(int32_t s1, int32_t s2, int32_t cols, int32_t M_ln, int32_t& f,
+                                         int32_t& muf) {
+  const int32_t as1 = s1 < 0 ? -s1 : s1;
+  const int32_t q1 = udiv_fast(as1, cols);
+  const int32_t mu = s1 >= 0 ? q1 : -q1 - (as1 - q1 * cols != 0 ? 1 : 0);
+  const int32_t V = udiv_fast(s2 - 2 * mu * s1 + cols * mu * mu, cols);
+  int32_t sigma = isqrt_newton10(V);
+  if (sigma < 1) sigma = 1;
+  f = udiv_fast(1 << M_ln, sigma);
+  muf = mu * f;
+}
+
+// the four normalised bytes of the word w of a row, requantised (not yet saturated)
+__device__ __forceinline__ void norm_word(uint32_t w, int32_t f, int32_t muf, int sh, const int4& g4, const int4& b4,
+                                          const NormArgs& n, int32_t lo, int32_t hi, int32_t (&r)[4]) {
+  const int32_t gg[4] = {g4.x, g4.y, g4.z, g4.w};
+  const int32_t bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int32_t nv = (sext_byte(w, e) * f - muf) >> sh;
+    const int32_t acc = nv * gg[e] + bb[e];
+    if (n.fast) {
+      r[e] = __mulhi(n.out_bq, acc);
+    } else {
+      const int64_t pr = (int64_t)n.out.b * min(max(acc, lo), hi);
+      r[e] = (int32_t)__funnelshift_r((uint32_t)pr, (uint32_t)(pr >> 32), (uint32_t)n.out.c);
+    }
+  }
+}
+
+template <int LPR>
+__device__ __forceinline__ void row_sum2(int32_t& s1, int32_t& s2) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) {
+    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+    s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+  }
+}
+
+// gamma (sign-extended), beta or the scale as 16-byte groups of four
+// channels, [q][chunk] as in layernorm_staged_kernel
+__device__ __forceinline__ void stage_gamma(int4* dst, const int8_t* g, int i, int nchunk) {
+  const uint32_t g4 = __ldg(reinterpret_cast<const uint32_t*>(g) + i);
+  dst[(i & 3) * nchunk + (i >> 2)] = make_int4(sext_byte(g4, 0), sext_byte(g4, 1), sext_byte(g4, 2), sext_byte(g4, 3));
+}
+__device__ __forceinline__ void stage_i32(int4* dst, const int32_t* t, int i, int nchunk) {
+  dst[(i & 3) * nchunk + (i >> 2)] = __ldg(reinterpret_cast<const int4*>(t) + i);
+}
+
+template <int LPR, int CPL, bool POST, bool PRE>
+__global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNormArgs a) {
+  extern __shared__ int4 ln_smem[];
+  const int cols = a.cols, nchunk = cols >> 4;
+  int4* const s_scale = ln_smem;  // [4][nchunk] each
+  int4* const s_pg = s_scale + 4 * nchunk;
+  int4* const s_pb = s_pg + (POST ? 4 * nchunk : 0);
+  int4* const s_ng = s_pb + (POST ? 4 * nchunk : 0);
+  int4* const s_nb = s_ng + (PRE ? 4 * nchunk : 0);
+  for (int i = threadIdx.x; i < cols / 4; i += blockDim.x) {
+    stage_i32(s_scale, a.scale, i, nchunk);
+    if (POST) {
+      stage_gamma(s_pg, a.post.gamma, i, nchunk);
+      stage_i32(s_pb, a.post.beta, i, nchunk);
+    }
+    if (PRE) {
+      stage_gamma(s_ng, a.pre.gamma, i, nchunk);
+      stage_i32(s_nb, a.pre.beta, i, nchunk);
+    }
+  }
+  __syncthreads();
+  pdl_wait();  // skip, branch and gate come from earlier kernels
+  pdl_launch_dependents();
+  const int hl = threadIdx.x % LPR;
+  constexpr int kRows = kLnThreads / LPR;
+  int32_t plo = INT_MIN, phi = INT_MAX, nlo = INT_MIN, nhi = INT_MAX;
+  if (POST && !a.post.fast) out_bounds(a.post.out.b, a.post.out.c, plo, phi);
+  if (PRE && !a.pre.fast) out_bounds(a.pre.out.b, a.pre.out.c, nlo, nhi);
+  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows; row0 += (int64_t)gridDim.x * kRows) {
+    const int64_t row = row0 + threadIdx.x / LPR;
+    const bool active = row < a.rows;
+    const int64_t base = (active ? row : 0) * cols;
+    const int4* xr = reinterpret_cast<const int4*>(a.skip + base);
+    const int4* br = reinterpret_cast<const int4*>(a.branch + base);
+    const int4* gr = a.gate ? reinterpret_cast<const int4*>(a.gate + (active ? row / a.gate_rows : 0) * cols) : nullptr;
+    int4 vx[CPL], vb[CPL];
+    int32_t s1 = 0, s2 = 0;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+      const int ci = hl + LPR * k;
+      if (active && ci < nchunk) {
+        vb[k] = __ldcs(br + ci);
+        vx[k] = __ldcs(xr + ci);
+        if (POST) {
+          const int w[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s1 = __dp4a(w[e], 0x01010101, s1);
+            s2 = __dp4a(w[e], w[e], s2);
+          }
+        }
+      }
+    }
+    int32_t f = 0, muf = 0;
+    if (POST) {
+      row_sum2<LPR>(s1, s2);
+      norm_row(s1, s2, cols, a.post.M_ln, f, muf);
+    }
+    const int psh = a.post.M_ln - a.post.F;
+    s1 = 0;
+    s2 = 0;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+      const int ci = hl + LPR * k;
+      if (active && ci < nchunk) {
+        const uint32_t bw[4] = {(uint32_t)vb[k].x, (uint32_t)vb[k].y, (uint32_t)vb[k].z, (uint32_t)vb[k].w};
+        const uint32_t xw[4] = {(uint32_t)vx[k].x, (uint32_t)vx[k].y, (uint32_t)vx[k].z, (uint32_t)vx[k].w};
+        int4 gv = make_int4(0x01010101, 0x01010101, 0x01010101, 0x01010101);
+        if (gr) gv = __ldg(gr + ci);
+        const uint32_t gw[4] = {(uint32_t)gv.x, (uint32_t)gv.y, (uint32_t)gv.z, (uint32_t)gv.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          int32_t u[4];
+          if (POST) {
+            norm_word(bw[q], f, muf, psh, s_pg[q * nchunk + ci], s_pb[q * nchunk + ci], a.post, plo, phi, u);
+            const uint32_t pw = pack_sat4_ln(u[0], u[1], u[2], u[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = sext_byte(pw, e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = sext_byte(bw[q], e);
+          }
+          const int4 s4 = s_scale[q * nchunk + ci];
+          const int32_t ss[4] = {s4.x, s4.y, s4.z, s4.w};
+          int32_t r[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // |sum| < 2^31 (2^7 + 2^14)
+            const int64_t t = (int64_t)a.b_skip * sext_byte(xw[q], e) + (int64_t)ss[e] * (u[e] * sext_byte(gw[q], e));
+            if (a.fast_res) {
+              r[e] = (int32_t)__funnelshift_r((uint32_t)t, (uint32_t)(t >> 32), (uint32_t)a.c);
+            } else {
+              const int64_t v = t >> a.c;
+              r[e] = (int32_t)(v < -128 ? -128 : (v > 127 ? 127 : v));
+            }
+          }
+          o[q] = pack_sat4_ln(r[0], r[1], r[2], r[3]);
+          if (PRE) {
+            s1 = __dp4a((int)o[q], 0x01010101, s1);
+            s2 = __dp4a((int)o[q], (int)o[q], s2);
+          }
+        }
+        vx[k] = make_int4((int)o[0], (int)o[1], (int)o[2], (int)o[3]);
+        __stcs(reinterpret_cast<int4*>(a.y + base) + ci, vx[k]);
+      }
+    }
+    if (PRE) {
+      row_sum2<LPR>(s1, s2);
+      norm_row(s1, s2, cols, a.pre.M_ln, f, muf);
+      const int nsh = a.pre.M_ln - a.pre.F;
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) {
+        const int ci = hl + LPR * k;
+        if (active && ci < nchunk) {
+          const uint32_t w[4] = {(uint32_t)vx[k].x, (uint32_t)vx[k].y, (uint32_t)vx[k].z, (uint32_t)vx[k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            int32_t r[4];
+            norm_word(w[q], f, muf, nsh, s_ng[q * nchunk + ci], s_nb[q * nchunk + ci], a.pre, nlo, nhi, r);
+            o[q] = pack_sat4_ln(r[0], r[1], r[2], r[3]);
+          }
+          __stcs(reinterpret_cast<int4*>(a.z + base) + ci, make_int4((int)o[0], (int)o[1], (int)o[2], (int)o[3]));
+        }
+      }
+    }
+  }
+}
+
 }  // namespace
+
+namespace {
+
+NormArgs norm_args(const ivit_norm* n) {
+  if (!n) return NormArgs{};
+  // the output requant is one mul.hi by b 2^(32 - c) when that fits a positive int32
+  const bool fast = n->out.c >= 1 && (int64_t)n->out.b < ((int64_t)1 << (n->out.c - 1));
+  return NormArgs{n->gamma, n->beta, n->F, n->M_ln, n->out, fast ? (int32_t)((int64_t)n->out.b << (32 - n->out.c)) : 0,
+                  fast ? 1 : 0};
+}
+
+template <int LPR, int CPL, bool POST, bool PRE>
+cudaError_t run_residual_norm(const DeviceCtx& dc, const ResNormArgs& a, cudaStream_t stream) {
+  constexpr int kRows = kLnThreads / LPR;
+  const size_t smem = (size_t)a.cols * 4 * (1 + (POST ? 2 : 0) + (PRE ? 2 : 0));  // at most 40 KB
+  auto kern = residual_norm_kernel<LPR, CPL, POST, PRE>;
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kLnThreads, smem) != cudaSuccess)
+    return cudaErrorUnknown;
+  int64_t blocks = (a.rows + kRows - 1) / kRows;
+  const int64_t cap = (int64_t)dc.num_sms * (per_sm > 0 ? per_sm : 1);
+  if (blocks > cap) blocks = cap;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(kLnThreads), smem, stream, a);
+}
+
+template <int LPR, int CPL>
+cudaError_t run_residual_norm_cpl(const DeviceCtx& dc, const ResNormArgs& a, bool post, bool pre, cudaStream_t stream) {
+  if (post) return pre ? run_residual_norm<LPR, CPL, true, true>(dc, a, stream) : run_residual_norm<LPR, CPL, true, false>(dc, a, stream);
+  return pre ? run_residual_norm<LPR, CPL, false, true>(dc, a, stream) : run_residual_norm<LPR, CPL, false, false>(dc, a, stream);
+}
+
+}  // namespace
+
+ivit_status launch_residual_norm(const DeviceCtx& dc, const int8_t* skip, const int8_t* branch, int64_t rows,
+                                 int32_t cols, const ivit_norm* post, const int8_t* gate, int64_t gate_rows,
+                                 const int32_t* scale, int32_t b_skip, int32_t c, const ivit_norm* pre, int8_t* y,
+                                 int8_t* z, cudaStream_t stream) {
+  if (rows == 0) return IVIT_OK;
+  // |b_skip x + scale u| < 2^38 + 2^31 |u|, |u| <= 2^7 or with a gate 2^14:
+  // shifted right by c >= 9 (gate: 15) it fits int32
+  const ResNormArgs a{skip, branch, rows, cols, norm_args(post), norm_args(pre), gate, gate ? gate_rows : 1, scale,
+                      b_skip, c, c >= (gate ? 15 : 9) ? 1 : 0, y, z};
+  const int cpl = (cols / 16 + kLnLanes - 1) / kLnLanes;
+  const bool po = post != nullptr, pr = pre != nullptr;
+  cudaError_t e;
+  if (cpl <= 1)
+    e = run_residual_norm_cpl<kLnLanes, 1>(dc, a, po, pr, stream);
+  else if (cpl <= 2)
+    e = run_residual_norm_cpl<kLnLanes, 2>(dc, a, po, pr, stream);
+  else if (cpl <= 3)
+    e = run_residual_norm_cpl<kLnLanes, 3>(dc, a, po, pr, stream);
+  else if (cpl <= 4)
+    e = run_residual_norm_cpl<kLnLanes, 4>(dc, a, po, pr, stream);
+  else if (cpl <= 6)
+    e = run_residual_norm_cpl<kLnLanes, 6>(dc, a, po, pr, stream);
+  else
+    e = run_residual_norm_cpl<kLnLanes, 8>(dc, a, po, pr, stream);
+  note_launch();
+  return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
+}
 
 ivit_status launch_shiftgelu_rowmax(const DeviceCtx& dc, const int8_t* x, int64_t rows, int32_t cols,
                                     const GeluParams& g, int8_t* y, cudaStream_t stream) {

@@ -51,6 +51,18 @@
 // stage, never two phases ahead of it (TMA loads may complete out of order,
 // and a parity wait cannot tell phase p from phase p + 2).  At BN = 256 the
 // ring is three deep and a single thread keeps the tensor core busy.
+//
+// Low-rank adapters of many requests (LORA, ivit_linear_lora): after a tile's
+// k-slices come its adapter stages.  t = requant(X A_a^T) [M x R] has been
+// written by the kernel before; request q's rows of it and its adapter's
+// B_a [N x R] are one more stretch of reduction, sum_r t_ir B_a[j, r], that
+// accumulates onto the same TMEM tile, so every epilogue applies unchanged.
+// The rows of other requests must not see B_a: t is loaded through a tensor
+// map [request, row of request, R], whose bounds zero-fill every token of the
+// tile outside request q, and a request without an adapter loads B_a from
+// outside the map, zero as well.  One ring stage holds up to four such
+// 32-byte chunks (32B swizzle, 128 x 32 B of B_a and BN x 32 B of t each), so
+// a tile of two or three requests of rank up to 32 pays for one stage.
 #include <climits>
 
 #include "ivit_common.cuh"
@@ -69,6 +81,7 @@ constexpr int kSlotBytes = 16 * kBM;  // one staged chunk: 16 tokens x 128 chann
 struct GemmArgs {
   int64_t M;       // tokens (rows of X and Y)
   int32_t N, K;    // output channels, reduction length
+  int32_t Kacc;    // products per accumulator: K, and the rank of an adapter beside it
   const int32_t* bias;
   const int32_t* b;
   const int8_t* c;
@@ -79,6 +92,50 @@ struct GemmArgs {
   int* status;
   int32_t withhold;  // diagnostic: CTA 0's producer stops before this k-slice of its sequence (-1: never)
 };
+
+// The adapter operands of a LORA launch (see above); empty without.
+constexpr int kLoraChunk = 32;           // bytes = rank entries per chunk, one MMA k-step
+constexpr int kLoraPerStage = kBK / kLoraChunk;
+template <bool LORA>
+struct LoraOperands {};
+template <>
+struct LoraOperands<true> {
+  CUtensorMap T;        // t: (R, rows, requests), box 32 x BN x 1
+  CUtensorMap B;        // B: (R, N, adapters), box 32 x 128 x 1
+  const int32_t* idx;   // adapter of each request
+  uint32_t rows;        // tokens per request
+  int32_t n;            // adapters
+  int32_t chunks;       // ceil(R / 32)
+};
+
+// First request and number of chunks (requests x rank chunks) of the token
+// tile [first, first + BN).
+template <int BN>
+IVIT_DEV void lora_span(const LoraOperands<true>& lo, int64_t M, int tb, uint32_t& q0, int& total) {
+  const uint32_t first = (uint32_t)tb * (uint32_t)BN;  // M < 2^31
+  const uint32_t last = min(first + (uint32_t)BN, (uint32_t)M) - 1u;
+  q0 = first / lo.rows;
+  total = (int)(last / lo.rows - q0 + 1u) * lo.chunks;
+}
+
+// Loads adapter stage k of the tile: chunks [4 k, 4 k + 4) of its span.
+template <int BN>
+IVIT_DEV void lora_load_stage(const LoraOperands<true>& lo, int k, int cb, int tb, uint32_t q0, int total,
+                              uint8_t* sa, int a_bytes, uint64_t* full) {
+  const int u0 = k * kLoraPerStage;
+  const int nu = min(kLoraPerStage, total - u0);
+  mbar_arrive_expect_tx(full, (uint32_t)(nu * (kBM + BN) * kLoraChunk));
+  for (int i = 0; i < nu; ++i) {
+    const int u = u0 + i;
+    const int r = u / lo.chunks, cc = u - r * lo.chunks;
+    const uint32_t q = q0 + (uint32_t)r;
+    int32_t a = __ldg(lo.idx + q);
+    if (a < 0 || a >= lo.n) a = -1;  // outside the map: B loads as zeros
+    tma_load_3d(sa + i * (kBM * kLoraChunk), &lo.B, cc * kLoraChunk, cb * kBM, a, full);
+    tma_load_3d(sa + a_bytes + i * (BN * kLoraChunk), &lo.T, cc * kLoraChunk,
+                (int32_t)((int64_t)tb * BN - (int64_t)q * lo.rows), (int32_t)q, full);
+  }
+}
 
 template <int BN, int STAGES>
 struct GemmLayout {
@@ -338,11 +395,11 @@ IVIT_DEV void bias_fill(uint32_t tbase, int c_begin, int c_end, int32_t bias) {
   for (int cc = c_begin; cc < c_end; ++cc) tmem_st16_fill(tbase + (uint32_t)(16 * cc), (uint32_t)bias);
 }
 
-template <int BN, int STAGES, int EPI, bool NARROW>
+template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_i8_requant_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                            const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS,
-                           const GemmArgs args) {
+                           const __grid_constant__ LoraOperands<LORA> lora, const GemmArgs args) {
   using L = GemmLayout<BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -380,6 +437,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmY);
     if (EPI == kEpiResidual) prefetch_tensormap(&tmS);
+    if constexpr (LORA) {
+      prefetch_tensormap(&lora.T);
+      prefetch_tensormap(&lora.B);
+    }
   }
   if (EPI == kEpiGelu) {
     for (int i = threadIdx.x; i < 256; i += blockDim.x)
@@ -407,7 +468,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int issued = 0;  // k-slices loaded so far by this CTA
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const int cb = t % ch_tiles, tb = t / ch_tiles;
-        for (int kb = 0; kb < num_kb; ++kb, ++issued) {
+        int tile_kb = num_kb;
+        [[maybe_unused]] uint32_t q0 = 0;
+        [[maybe_unused]] int lora_total = 0;
+        if constexpr (LORA) {
+          lora_span<BN>(lora, M, tb, q0, lora_total);
+          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
+        }
+        for (int kb = 0; kb < tile_kb; ++kb, ++issued) {
           if (!mbar_wait(&empty[stage], phase ^ 1, args.status)) {
             ok = false;
             break;
@@ -418,10 +486,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
           uint8_t* sa = smem + stage * L::kStageBytes;
-          tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
-          tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
+          if (LORA && kb >= num_kb) {
+            if constexpr (LORA)
+              lora_load_stage<BN>(lora, kb - num_kb, cb, tb, q0, lora_total, sa, L::kABytes, &full[stage]);
+          } else {
+            mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
+            tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
+            tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
+          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -439,6 +512,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // loop stays a handful of instructions per MMA
       const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint32_t d_lo0 = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
+      // adapter chunks: rows of 32 bytes, 8-row groups of 256 bytes; the low
+      // half (start address, leading offset) is that of the k-slices
+      [[maybe_unused]] const uint32_t d_hi32 = (uint32_t)(smem_desc(0, 16, 256, kSwizzle32B) >> 32);
       // this thread takes every kStep-th k-slice of the CTA's sequence,
       // starting with slice warp - 1; the ring position advances kStep stages
       // per slice
@@ -453,8 +529,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!mbar_wait(&tempty[acc], acc_phase, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * L::kAccCols);
+        int tile_kb = num_kb;
+        [[maybe_unused]] int lora_total = 0;
+        if constexpr (LORA) {
+          uint32_t q0;
+          lora_span<BN>(lora, M, t / ch_tiles, q0, lora_total);
+          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
+        }
         int kb = kb0;
-        for (; kb < num_kb; kb += kStep) {
+        for (; kb < tile_kb; kb += kStep) {
           if (!mbar_wait(&full[stage], phase, args.status)) {
             ok = false;
             break;
@@ -462,9 +545,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tc_fence_after();
           const uint32_t a_lo = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
           const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
+          if (LORA && kb >= num_kb) {
+            const int nu = min(kLoraPerStage, lora_total - (kb - num_kb) * kLoraPerStage);
+            for (int i = 0; i < nu; ++i)
+              umma_i8_acc(d_tmem, a_lo + i * (kBM * kLoraChunk >> 4), d_hi32, b_lo + i * (BN * kLoraChunk >> 4),
+                          d_hi32, idesc);
+          } else {
 #pragma unroll
-          for (int k = 0; k < kBK / 32; ++k)  // accumulate onto the preloaded bias
-            umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
+            for (int k = 0; k < kBK / 32; ++k)  // accumulate onto the preloaded bias
+              umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
+          }
           umma_commit(&empty[stage]);
           stage += kStep;
           if (stage >= STAGES) {
@@ -473,7 +563,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         }
         if (!ok) break;
-        kb0 = kb - num_kb;
+        kb0 = kb - tile_kb;
         // arrives once this thread's MMAs of the tile (possibly none) are done
         umma_commit(&tfull[acc]);
         acc ^= 1;
@@ -546,7 +636,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       cb_bias = (ok && args.bias) ? __ldg(args.bias + chx) : 0;
     };
     auto derive = [&](int cbx, int32_t vb, int32_t vc, int32_t vbias, ChanConst& kx, int& reqx) {
-      kx = cbx * kBM + quarter * 32 + lane < N ? chan_const(vb, vc, vbias, args.K) : chan_const(0, 0, 0, args.K);
+      kx = cbx * kBM + quarter * 32 + lane < N ? chan_const(vb, vc, vbias, args.Kacc) : chan_const(0, 0, 0, args.Kacc);
       // warp-uniform requant form
       reqx = __all_sync(0xffffffffu, kx.fast) ? kReqFast
                                                : (__any_sync(0xffffffffu, kx.needs_clamp) ? kReqWideClamp : kReqWide);
@@ -687,11 +777,11 @@ struct OwnLayout {
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
 
-template <int BN, int STAGES, int EPI, bool NARROW>
+template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_own_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS,
-                    const GemmArgs args) {
+                    const __grid_constant__ LoraOperands<LORA> lora, const GemmArgs args) {
   using L = OwnLayout<BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -729,6 +819,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmY);
     if (EPI == kEpiResidual) prefetch_tensormap(&tmS);
+    if constexpr (LORA) {
+      prefetch_tensormap(&lora.T);
+      prefetch_tensormap(&lora.B);
+    }
   }
   if (EPI == kEpiGelu) {
     for (int i = threadIdx.x; i < 256; i += blockDim.x)
@@ -756,7 +850,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int issued = 0;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const int cb = t % ch_tiles, tb = t / ch_tiles;
-        for (int kb = 0; kb < num_kb; ++kb, ++issued) {
+        int tile_kb = num_kb;
+        [[maybe_unused]] uint32_t q0 = 0;
+        [[maybe_unused]] int lora_total = 0;
+        if constexpr (LORA) {
+          lora_span<BN>(lora, M, tb, q0, lora_total);
+          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
+        }
+        for (int kb = 0; kb < tile_kb; ++kb, ++issued) {
           if (!mbar_wait(&empty[stage], phase ^ 1, args.status)) {
             ok = false;
             break;
@@ -765,10 +866,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
           uint8_t* sa = smem + stage * L::kStageBytes;
-          tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
-          tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
+          if (LORA && kb >= num_kb) {
+            if constexpr (LORA)
+              lora_load_stage<BN>(lora, kb - num_kb, cb, tb, q0, lora_total, sa, L::kABytes, &full[stage]);
+          } else {
+            mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
+            tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
+            tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
+          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -783,6 +889,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t idesc = idesc_i8(kBM, BN, true, true, false);
       const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint32_t d_lo0 = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
+      // adapter chunks: rows of 32 bytes, 8-row groups of 256 bytes; the low
+      // half (start address, leading offset) is that of the k-slices
+      [[maybe_unused]] const uint32_t d_hi32 = (uint32_t)(smem_desc(0, 16, 256, kSwizzle32B) >> 32);
       int stage = warp - 1;
       uint32_t phase = 0;
       int kb0 = warp - 1;
@@ -793,8 +902,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!mbar_wait(&tempty[acc], acc_phase, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * L::kAccCols);
+        int tile_kb = num_kb;
+        [[maybe_unused]] int lora_total = 0;
+        if constexpr (LORA) {
+          uint32_t q0;
+          lora_span<BN>(lora, M, t / ch_tiles, q0, lora_total);
+          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
+        }
         int kb = kb0;
-        for (; kb < num_kb; kb += kStep) {
+        for (; kb < tile_kb; kb += kStep) {
           if (!mbar_wait(&full[stage], phase, args.status)) {
             ok = false;
             break;
@@ -802,8 +918,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tc_fence_after();
           const uint32_t a_lo = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
           const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
+          if (LORA && kb >= num_kb) {
+            const int nu = min(kLoraPerStage, lora_total - (kb - num_kb) * kLoraPerStage);
+            for (int i = 0; i < nu; ++i)
+              umma_i8_acc(d_tmem, a_lo + i * (kBM * kLoraChunk >> 4), d_hi32, b_lo + i * (BN * kLoraChunk >> 4),
+                          d_hi32, idesc);
+          } else {
 #pragma unroll
-          for (int k = 0; k < kBK / 32; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
+            for (int k = 0; k < kBK / 32; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
+          }
           umma_commit(&empty[stage]);
           stage += kStep;
           if (stage >= STAGES) {
@@ -812,7 +935,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         }
         if (!ok) break;
-        kb0 = kb - num_kb;
+        kb0 = kb - tile_kb;
         umma_commit(&tfull[acc]);
         if (++acc == kOwnAcc) {
           acc = 0;
@@ -860,7 +983,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       vbias = (okc && args.bias) ? __ldg(args.bias + ch) : 0;
     };
     auto derive = [&](int tt, int32_t vb, int32_t vc, int32_t vbias, ChanConst& kx, int& reqx) {
-      kx = chan_of(tt) < N ? chan_const(vb, vc, vbias, args.K) : chan_const(0, 0, 0, args.K);
+      kx = chan_of(tt) < N ? chan_const(vb, vc, vbias, args.Kacc) : chan_const(0, 0, 0, args.Kacc);
       reqx = __all_sync(0xffffffffu, kx.fast) ? kReqFast
                                               : (__any_sync(0xffffffffu, kx.needs_clamp) ? kReqWideClamp : kReqWide);
     };
@@ -945,9 +1068,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-template <int BN, int STAGES, int EPI, bool NARROW>
+// The adapter operands of one launch from the caller's adapters.
+template <int BN>
+ivit_status encode_lora(const GemmArgs& a, const LoraGemm* lg, LoraOperands<true>* lo) {
+  const uint64_t R = (uint64_t)lg->R;
+  ivit_status st = encode_tmap_3d_u8(&lo->T, lg->T, R, lg->rows, (uint64_t)a.M / lg->rows, kLoraChunk, BN,
+                                     CU_TENSOR_MAP_SWIZZLE_32B);
+  if (st != IVIT_OK) return st;
+  st = encode_tmap_3d_u8(&lo->B, lg->B, R, (uint64_t)a.N, (uint64_t)lg->n, kLoraChunk, kBM, CU_TENSOR_MAP_SWIZZLE_32B);
+  lo->idx = lg->idx;
+  lo->rows = (uint32_t)lg->rows;
+  lo->n = lg->n;
+  lo->chunks = (lg->R + kLoraChunk - 1) / kLoraChunk;
+  return st;
+}
+template <int BN>
+ivit_status encode_lora(const GemmArgs&, const LoraGemm*, LoraOperands<false>*) {
+  return IVIT_OK;
+}
+
+template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
 ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
-                         const GemmArgs& a, cudaStream_t stream) {
+                         const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
   using L = OwnLayout<BN, STAGES>;
   CUtensorMap tmW, tmX, tmY, tmS;
   ivit_status st = encode_tmap_2d_u8(&tmW, W, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.K, kBK, kBM,
@@ -964,23 +1106,25 @@ ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, 
   } else {
     tmS = tmY;  // unused
   }
-  auto kern = gemm_own_kernel<BN, STAGES, EPI, NARROW>;
-  static bool attr_done = false;  // benign race: the attribute value is the same
-  if (!attr_done) {
+  LoraOperands<LORA> lora;
+  if ((st = encode_lora<BN>(a, lg, &lora)) != IVIT_OK) return st;
+  auto kern = gemm_own_kernel<BN, STAGES, EPI, NARROW, LORA>;
+  static bool attr_done[64];  // per device; benign race: the attribute value is the same
+  if (!attr_done[dc.device]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
       return IVIT_ERR_CUDA;
-    attr_done = true;
+    attr_done[dc.device] = true;
   }
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kGemmThreads), L::kAlloc, stream, tmW, tmX, tmY, tmS, a);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kGemmThreads), L::kAlloc, stream, tmW, tmX, tmY, tmS, lora, a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
 
-template <int BN, int STAGES, int EPI, bool NARROW>
+template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
 ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
-                     const GemmArgs& a, cudaStream_t stream) {
+                     const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
   using L = GemmLayout<BN, STAGES>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory budget");
   CUtensorMap tmW, tmX, tmY, tmS;
@@ -999,16 +1143,18 @@ ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, cons
   } else {
     tmS = tmY;  // unused
   }
-  auto kern = gemm_i8_requant_kernel<BN, STAGES, EPI, NARROW>;
-  static bool attr_done = false;  // benign race: the attribute value is the same
-  if (!attr_done) {
+  LoraOperands<LORA> lora;
+  if ((st = encode_lora<BN>(a, lg, &lora)) != IVIT_OK) return st;
+  auto kern = gemm_i8_requant_kernel<BN, STAGES, EPI, NARROW, LORA>;
+  static bool attr_done[64];  // per device; benign race: the attribute value is the same
+  if (!attr_done[dc.device]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
       return IVIT_ERR_CUDA;
-    attr_done = true;
+    attr_done[dc.device] = true;
   }
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kGemmThreads), L::kAlloc, stream, tmW, tmX, tmY, tmS, a);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kGemmThreads), L::kAlloc, stream, tmW, tmX, tmY, tmS, lora, a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
@@ -1070,32 +1216,32 @@ bool use_own_tiles(int K) {
   return K <= 512 || (EPI == kEpiGelu && K <= 768);
 }
 
-template <int EPI, bool NARROW>
+template <int EPI, bool NARROW, bool LORA>
 ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
-                        const GemmArgs& a, cudaStream_t stream) {
+                        const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
   if (use_own_tiles<EPI>(a.K)) {
     switch (pick_bn_own(a.M, a.N, dc.num_sms)) {
       case 160:
-        return run_gemm_own<160, 4, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+        return run_gemm_own<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 144:
-        return run_gemm_own<144, 4, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+        return run_gemm_own<144, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       default:
-        return run_gemm_own<128, 4, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+        return run_gemm_own<128, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     }
   }
   switch (pick_bn(a.M, a.N, dc.num_sms)) {
     case 256:
-      return run_gemm<256, 3, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+      return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     case 224:
-      return run_gemm<224, 4, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+      return run_gemm<224, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     case 192:
-      return run_gemm<192, 4, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+      return run_gemm<192, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     case 176:
-      return run_gemm<176, 4, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+      return run_gemm<176, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     case 160:
-      return run_gemm<160, 4, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+      return run_gemm<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     default:
-      return run_gemm<128, 6, EPI, NARROW>(dc, X, W, skip, Y, a, stream);
+      return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
   }
 }
 
@@ -1104,12 +1250,13 @@ ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, c
 ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
                         const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits, bool round,
                         EpiMode mode, const int8_t* skip, ivit_residual res, const GeluParams* gelu, int8_t* Y,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, const LoraGemm* lora) {
   GemmArgs a;
   a.round = round ? 1 : 0;
   a.M = M;
   a.N = N;
   a.K = K;
+  a.Kacc = K + (lora ? lora->R : 0);
   a.bias = bias;
   a.b = b;
   a.c = c;
@@ -1120,16 +1267,18 @@ ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t
   a.status = dc.status;
   a.withhold = take_withhold(kWithholdGemm);
   const bool narrow = out_bits < 8;
+#define IVIT_GEMM_DISPATCH(EPI, NARROW)                                              \
+  (lora ? dispatch_bn<EPI, NARROW, true>(dc, X, W, skip, Y, a, lora, stream)         \
+        : dispatch_bn<EPI, NARROW, false>(dc, X, W, skip, Y, a, nullptr, stream))
   switch (mode) {
     case kEpiPlain:
-      return narrow ? dispatch_bn<kEpiPlain, true>(dc, X, W, skip, Y, a, stream)
-                    : dispatch_bn<kEpiPlain, false>(dc, X, W, skip, Y, a, stream);
+      return narrow ? IVIT_GEMM_DISPATCH(kEpiPlain, true) : IVIT_GEMM_DISPATCH(kEpiPlain, false);
     case kEpiResidual:
-      return narrow ? dispatch_bn<kEpiResidual, true>(dc, X, W, skip, Y, a, stream)
-                    : dispatch_bn<kEpiResidual, false>(dc, X, W, skip, Y, a, stream);
+      return narrow ? IVIT_GEMM_DISPATCH(kEpiResidual, true) : IVIT_GEMM_DISPATCH(kEpiResidual, false);
     case kEpiGelu:
-      return dispatch_bn<kEpiGelu, false>(dc, X, W, skip, Y, a, stream);
+      return IVIT_GEMM_DISPATCH(kEpiGelu, false);
   }
+#undef IVIT_GEMM_DISPATCH
   return IVIT_ERR_INTERNAL;
 }
 

@@ -55,14 +55,35 @@ ivit_status encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner
                               uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
                               CUtensorMapSwizzle swizzle);
 
+// The same for a contiguous [d2 x d1 x d0] byte tensor with boxes of
+// box0 x box1 x 1 (d0 a multiple of 16).
+ivit_status encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                              uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle);
+
 // The host-side checks of one encoder-block call other than those of its
 // workspace (parameters, alignment, sizes, attention configuration).
 ivit_status check_block_args(const ivit_block_params* p, const int8_t* x, const int8_t* y, int32_t B, int32_t N);
 
+// Low-rank adapters beside a GEMM: request q = rows [q * rows, (q + 1) * rows)
+// of X adds t B_a^T, a = idx[q], to its accumulators.
+struct LoraGemm {
+  const int8_t* T;     // [M x R], written by launch_lora_down
+  const int8_t* B;     // [n x N x R]
+  const int32_t* idx;  // [M / rows]; outside [0, n): no adapter
+  int32_t n, R;
+  int64_t rows;
+};
+
+// t = sat_8((b_t (X A_a^T)) >> c_t) [M x R] of every request with an adapter
+// (the rows of the others are left as they were).
+ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* A,
+                             const int32_t* b_t, const int8_t* c_t, bool round, const LoraGemm& lora, int8_t* T,
+                             cudaStream_t stream);
+
 ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
                         const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits, bool round,
                         EpiMode mode, const int8_t* skip, ivit_residual res, const GeluParams* gelu, int8_t* Y,
-                        cudaStream_t stream);
+                        cudaStream_t stream, const LoraGemm* lora = nullptr);
 
 // Whether the attention kernels take (N, k_s, I0): up to 640 keys; logits
 // wider than 8 bits (ShiftExp computed, not looked up) on up to 256 keys and
@@ -101,6 +122,13 @@ ivit_status launch_tokens(const DeviceCtx& dc, const int8_t* e, const int8_t* cl
 // t [B x D] = the first of each image's Ntok rows of x (D a multiple of 16).
 ivit_status launch_gather_rows(const DeviceCtx& dc, const int8_t* x, int32_t B, int32_t Ntok, int32_t D, int8_t* t,
                                cudaStream_t stream);
+
+// A branch's end: y = skip and the branch (post-normed, gated, scaled) added,
+// z = the next norm of y (post, gate and pre optional; cols as above).
+ivit_status launch_residual_norm(const DeviceCtx& dc, const int8_t* skip, const int8_t* branch, int64_t rows,
+                                 int32_t cols, const ivit_norm* post, const int8_t* gate, int64_t gate_rows,
+                                 const int32_t* scale, int32_t b_skip, int32_t c, const ivit_norm* pre, int8_t* y,
+                                 int8_t* z, cudaStream_t stream);
 
 ivit_status launch_layernorm(const DeviceCtx& dc, const int8_t* x, int64_t rows, int32_t cols,
                              const int8_t* gamma, const int32_t* beta, int32_t F, int32_t M_ln, ivit_dyadic out,

@@ -1,0 +1,278 @@
+"""GPU parity of the serving operators against their plain 64-bit forms, bit
+for bit (every quantity is an integer): linear layers with a low-rank adapter
+per request, the end of a residual branch.  Outputs sit between canary bytes."""
+import numpy as np
+import pytest
+import torch
+
+import integer_only_quantized_int8_b200 as ivit
+from integer_only_quantized_int8_b200 import build as ivit_build
+from oracle import serving
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 4096
+CANARY = 0x5A
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ivit_build.build()
+    yield
+    assert ivit.ivit_stream_status() == 0
+
+
+def dev(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.cpu().numpy()
+
+
+def guarded(shape):
+    n = int(np.prod(shape))
+    buf = torch.full((n + 2 * GUARD,), CANARY, dtype=torch.uint8, device="cuda")
+    view = buf[GUARD:GUARD + n].view(torch.int8).view(shape)
+
+    def untouched():
+        h = host(buf)
+        return bool((h[:GUARD] == CANARY).all() and (h[GUARD + n:] == CANARY).all())
+
+    return view, untouched
+
+
+def rng_i8(r, *shape):
+    return r.integers(-128, 128, shape, dtype=np.int8)
+
+
+def workspace(M, R):
+    """A workspace full of stale bytes."""
+    return torch.full((ivit.ivit_linear_lora_workspace_bytes(M, R),), CANARY, dtype=torch.uint8, device="cuda")
+
+
+# ---------------------------------------------------------------- adapters
+
+class LoraCase:
+    """Inputs whose accumulators spread over the output range; wild: multipliers over their whole range."""
+
+    def __init__(self, req, rows, K, N, R, n, seed, wild=False, idx=None):
+        r = np.random.default_rng(seed)
+        self.M, self.rows, self.R = req * rows, rows, R
+        self.X, self.W = rng_i8(r, self.M, K), rng_i8(r, N, K)
+        A, B = rng_i8(r, n, R, K), rng_i8(r, n, N, R)
+        acc = 74.0 * 74.0 * np.sqrt(K)
+        self.bias = (r.standard_normal(N) * acc / 4).astype(np.int32)
+        if wild:
+            self.b, self.c = r.integers(0, 1 << 31, N).astype(np.int32), r.integers(0, 32, N).astype(np.int8)
+            b_t, c_t = r.integers(0, 1 << 31, (n, R)).astype(np.int32), r.integers(0, 32, (n, R)).astype(np.int8)
+        else:
+            c = int(min(31, 30 + np.log2(acc / 60)))
+            self.b = (r.uniform(0.5, 1.0, N) * 60 / acc * 2.0 ** c).astype(np.int32)
+            self.c = np.full(N, c, np.int8)
+            b_t = (r.uniform(0.5, 1.0, (n, R)) * 60 / acc * 2.0 ** c).astype(np.int32)
+            c_t = np.full((n, R), c, np.int8)
+        self.adapters = (A, b_t, c_t, B)
+        self.idx = r.integers(-1, n + 1, req).astype(np.int32) if idx is None else np.asarray(idx, np.int32)
+        self.skip = rng_i8(r, self.M, N)
+
+    def device(self):
+        return [dev(t) for t in (self.X, self.W, self.bias, self.b, self.c)] + [tuple(dev(t) for t in self.adapters),
+                                                                              dev(self.idx), self.rows]
+
+    def host(self):
+        return [self.X, self.W, self.bias, self.b, self.c, self.adapters, self.idx, self.rows]
+
+
+GELU = (27, 30, 8, (1476395008, 27))
+
+LORA_SHAPES = [
+    (1, 1, 16, 16, 16, 1), (3, 1, 144, 48, 16, 2), (130, 1, 96, 144, 16, 7), (300, 1, 768, 80, 48, 40),
+    (5, 7, 48, 80, 32, 3), (33, 9, 640, 272, 128, 5), (2, 197, 192, 576, 16, 4), (3, 130, 768, 144, 48, 2),
+    (1, 300, 384, 128, 112, 3), (2, 128, 128, 256, 64, 2), (7, 64, 1040, 1008, 16, 9), (2, 640, 2048, 192, 80, 2),
+]
+
+
+@pytest.mark.parametrize("req,rows,K,N,R,n", LORA_SHAPES)
+@pytest.mark.parametrize("epi", ["plain", "residual", "gelu"])
+def test_linear_lora_parity(req, rows, K, N, R, n, epi):
+    q = LoraCase(req, rows, K, N, R, n, seed=req + rows + K + N + R)
+    for rounding in (0, 1):
+        y, untouched = guarded((q.M, N))
+        if epi == "gelu":
+            ivit.ivit_linear_lora_shiftgelu(*q.device(), *GELU, y, workspace(q.M, R), rounding=rounding)
+            want = serving.linear_lora(*q.host(), rounding=rounding, gelu=GELU)
+        else:
+            res = (1 << 29, (1 << 28) + 77, 30) if epi == "residual" else None
+            skip = q.skip if epi == "residual" else None
+            bits = 8 - 2 * rounding
+            ivit.ivit_linear_lora(*q.device(), y, workspace(q.M, R), bits, dev(skip), res, rounding=rounding)
+            want = serving.linear_lora(*q.host(), bits, skip, res, rounding)
+        np.testing.assert_array_equal(host(y), want)
+        assert untouched()
+
+
+@pytest.mark.parametrize("req,rows,K,N,R,n", [(40, 1, 96, 272, 32, 5), (4, 70, 208, 144, 48, 3), (2, 200, 784, 160, 16, 2)])
+@pytest.mark.parametrize("rounding", [0, 1])
+def test_linear_lora_multipliers_of_every_size(req, rows, K, N, R, n, rounding):
+    q = LoraCase(req, rows, K, N, R, n, seed=7, wild=True)
+    q.bias[::3] = np.where(np.arange(len(q.bias[::3])) % 2, -(1 << 30), 1 << 30)
+    y, untouched = guarded((q.M, N))
+    ivit.ivit_linear_lora(*q.device(), y, workspace(q.M, R), rounding=rounding)
+    np.testing.assert_array_equal(host(y), serving.linear_lora(*q.host(), rounding=rounding))
+    assert untouched()
+
+
+@pytest.mark.parametrize("rows", [1, 37])
+@pytest.mark.parametrize("x,a", [(-128, -128), (-128, 127)])
+def test_linear_lora_largest_sums(rows, x, a):
+    """Every product of one sign: |t| saturates, the accumulator takes 2^14 (K + R)."""
+    q = LoraCase(3, rows, 2048, 64, 128, 2, seed=8, idx=[1, 0, 1])
+    q.X[:], q.W[:] = x, a
+    A, b_t, c_t, B = q.adapters
+    A[:], b_t[:], c_t[:], B[:] = a, (1 << 31) - 1, 0, a
+    q.b[:], q.c[:] = 5, 21
+    y, _ = guarded((q.M, 64))
+    ivit.ivit_linear_lora(*q.device(), y, workspace(q.M, 128))
+    np.testing.assert_array_equal(host(y), serving.linear_lora(*q.host()))
+
+
+@pytest.mark.parametrize("idx", [[-1, -1, -1, -1], [2, 2, 2, 2], [3, -(1 << 31), (1 << 31) - 1, 0]])
+@pytest.mark.parametrize("rows", [1, 65])
+def test_linear_lora_indexes(idx, rows):
+    """No adapter anywhere, one adapter for all, indexes far outside."""
+    q = LoraCase(4, rows, 160, 96, 16, 3, seed=9, idx=idx)
+    y, _ = guarded((q.M, 96))
+    ivit.ivit_linear_lora(*q.device(), y, workspace(q.M, 16))
+    np.testing.assert_array_equal(host(y), serving.linear_lora(*q.host()))
+
+
+def test_linear_lora_without_bias_and_without_rank():
+    """bias NULL; an adapter whose down projections are zero rows adds nothing."""
+    q = LoraCase(3, 50, 96, 112, 32, 2, seed=10, idx=[0, 1, 0])
+    q.bias = None
+    q.adapters[0][1] = 0
+    d = q.device()
+    y, _ = guarded((q.M, 112))
+    ivit.ivit_linear_lora(*d, y, workspace(q.M, 32))
+    np.testing.assert_array_equal(host(y), serving.linear_lora(*q.host()))
+    base = torch.empty_like(y)
+    ivit.ivit_linear_requant(*d[:5], base)
+    np.testing.assert_array_equal(host(y)[50:100], host(base)[50:100])
+
+
+def test_linear_lora_workspace_use():
+    """Only t's bytes are written, and only those of requests with an adapter."""
+    q = LoraCase(3, 20, 96, 112, 16, 2, seed=11, idx=[0, -1, 1])
+    ws = workspace(q.M + 64, 16)
+    y, _ = guarded((q.M, 112))
+    ivit.ivit_linear_lora(*q.device(), y, ws)
+    h = host(ws)
+    assert (h[20 * 16:40 * 16] == CANARY).all() and (h[60 * 16:] == CANARY).all()
+
+
+def test_linear_lora_capture_and_streams():
+    """A captured call replays on new inputs; two streams with a workspace each do not disturb one another."""
+    qs = [LoraCase(6, 33, 384, 256, 32, 4, seed=s) for s in (12, 13)]
+    want = [serving.linear_lora(*q.host()) for q in qs]
+    d = [q.device() for q in qs]
+    ys, wss = [guarded((qs[0].M, 256))[0] for _ in qs], [workspace(qs[0].M, 32) for _ in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            ivit.ivit_linear_lora(*d[i], ys[i], wss[i], stream=s)
+    for y, w in zip(ys, want):
+        np.testing.assert_array_equal(host(y), w)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ivit.ivit_linear_lora(*d[0], ys[0], wss[0])
+    d[0][0].copy_(d[1][0])
+    d[0][6].copy_(d[1][6])
+    qs[0].X, qs[0].idx = qs[1].X, qs[1].idx
+    for _ in range(2):
+        ys[0].zero_()
+        g.replay()
+        np.testing.assert_array_equal(host(ys[0]), serving.linear_lora(*qs[0].host()))
+
+
+# ---------------------------------------------------------------- the end of a branch
+
+def norm_params(r, cols, wild=False):
+    g = rng_i8(r, cols)
+    be = r.integers(-(1 << 30), (1 << 30) + 1, cols, dtype=np.int32) if wild else \
+        r.integers(-3000, 3000, cols, dtype=np.int32)
+    if wild:
+        F = int(r.integers(0, 15))
+        return g, be, F, int(r.integers(F, 24)), (int(r.integers(0, 1 << 31)), int(r.integers(0, 32)))
+    return g, be, 7, 23, (1466015503, 38 - 7)
+
+
+def dev_norm(n):
+    return None if n is None else (dev(n[0]), dev(n[1])) + tuple(n[2:])
+
+
+def branch_end(rows, cols, T, post, gate, pre, seed, wild=False, inplace=False):
+    r = np.random.default_rng(seed)
+    x, o = rng_i8(r, rows, cols), rng_i8(r, rows, cols)
+    o[0] = 17                                            # a row without variance
+    pp, np_ = (norm_params(r, cols, wild) if f else None for f in (post, pre))
+    g = rng_i8(r, -(-rows // T), cols) if gate else None
+    if wild:
+        scale = r.integers(-(1 << 31), 1 << 31, cols).astype(np.int32)
+        scale[:2] = -(1 << 31), (1 << 31) - 1
+        b_skip, c = int(r.integers(0, 1 << 31)), int(r.integers(0, 32))
+    else:
+        scale = (r.standard_normal(cols) * (4e6 if gate else 2.5e8)).astype(np.int32)
+        b_skip, c = 939524096, 30
+    want = serving.residual_norm(x, o, scale, b_skip, c, pp, g, T, np_)
+    y, ok_y = guarded((rows, cols))
+    z, ok_z = guarded((rows, cols)) if pre else (None, lambda: True)
+    dx, do = dev(x), dev(o)
+    if inplace:
+        y, z = dx, (do if pre else None)
+    got = ivit.ivit_residual_norm(dx, do, dev(scale), b_skip, c, y, dev_norm(pp), dev(g), T, dev_norm(np_), z)
+    for a, b in zip(got, want):
+        assert (a is None) == (b is None)
+        if a is not None:
+            np.testing.assert_array_equal(host(a), b)
+    assert ok_y() and ok_z()
+
+
+@pytest.mark.parametrize("rows,cols,T", [(1, 16, 1), (5, 48, 2), (197, 192, 197), (394, 768, 197), (130, 1024, 7),
+                                         (9, 2048, 9), (2500, 320, 50), (3, 528, 1), (64, 1296, 16), (33, 784, 40)])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("pre", [True, False])
+def test_residual_norm_parity(rows, cols, T, post, gate, pre):
+    branch_end(rows, cols, T, post, gate, pre, seed=rows + cols)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_residual_norm_parameters_of_every_size(seed):
+    r = np.random.default_rng(seed)
+    branch_end(int(r.integers(1, 90)), 16 * int(r.integers(1, 129)), int(r.integers(1, 20)), seed % 2 == 0, seed % 3 != 0,
+               seed % 5 != 0, seed=100 + seed, wild=True)
+
+
+@pytest.mark.parametrize("pre", [True, False])
+def test_residual_norm_in_place(pre):
+    branch_end(300, 384, 100, True, True, pre, seed=5, inplace=True)
+
+
+def test_residual_norm_capture_and_empty():
+    r = np.random.default_rng(6)
+    x, o = rng_i8(r, 40, 96), rng_i8(r, 40, 96)
+    scale, pre = r.integers(-(1 << 28), 1 << 28, 96).astype(np.int32), norm_params(r, 96)
+    dx, do, ds, dp = dev(x), dev(o), dev(scale), dev_norm(pre)
+    y, z = torch.empty_like(dx), torch.empty_like(dx)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ivit.ivit_residual_norm(dx, do, ds, 1 << 29, 30, y, pre=dp, z=z)
+    dx.copy_(do)
+    g.replay()
+    want = serving.residual_norm(o, o, scale, 1 << 29, 30, pre=pre)
+    np.testing.assert_array_equal(host(y), want[0])
+    np.testing.assert_array_equal(host(z), want[1])
+    ivit.ivit_residual_norm(dx[:0], do[:0], ds, 1, 0, y[:0], pre=dp, z=z[:0])

@@ -1,0 +1,125 @@
+"""Refusals of the serving operators, without a GPU: the binding's size checks
+(host tensors stop at "must be a CUDA tensor") and the library's own checks
+(no device pointer is touched before a failed one)."""
+import ctypes as C
+
+import pytest
+import torch
+
+import integer_only_quantized_int8_b200 as ivit
+from integer_only_quantized_int8_b200 import build as ivit_build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ivit_build.build()
+
+
+def i8(*shape):
+    return torch.zeros(shape, dtype=torch.int8)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def refused(fn, *a, **k):
+    with pytest.raises(ValueError, match="holds|shape"):
+        fn(*a, **k)
+
+
+def past_checks(fn, *a, **k):
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        fn(*a, **k)
+
+
+P = 0x100000
+D = ivit.Dyadic(1, 0)
+NONE = ivit.Residual(0, 0, 0)
+
+
+def test_linear_lora_sizes():
+    M, K, N, R, n = 32, 64, 48, 16, 3
+    ws = torch.zeros(M * R, dtype=torch.uint8)
+
+    def call(X=i8(M, K), W=i8(N, K), b=i32(N), A=i8(n, R, K), bt=i32(n, R), ct=i8(n, R), B=i8(n, N, R), idx=i32(4),
+             rows=8, Y=i8(M, N), skip=None):
+        return (ivit.ivit_linear_lora, X, W, None, b, i8(N), (A, bt, ct, B), idx, rows, Y, ws, 8, skip, (1, 1, 1))
+
+    past_checks(*call())
+    past_checks(*call(skip=i8(M, N)))
+    for bad in (dict(W=i8(N, K + 16)), dict(b=i32(N - 1)), dict(A=i8(n, R, K - 16)), dict(bt=i32(n * R - 1)),
+                dict(ct=i8(n, R - 1)), dict(B=i8(n - 1, N, R)), dict(B=i8(n, N - 16, R)), dict(idx=i32(3)),
+                dict(rows=5), dict(rows=0), dict(rows=-8), dict(Y=i8(M, N - 16)), dict(skip=i8(M - 1, N))):
+        refused(*call(**bad))
+    X, W, t, ad = i8(M, K), i8(N, K), (i32(N), i32(N), i8(N)), (i8(n, R, K), i32(n, R), i8(n, R), i8(n, N, R))
+    past_checks(ivit.ivit_linear_lora_shiftgelu, X, W, *t, ad, i32(4), 8, 4, 30, 8, (1, 0), i8(M, N), ws)
+    refused(ivit.ivit_linear_lora_shiftgelu, X, W, *t, ad, i32(4), 7, 4, 30, 8, (1, 0), i8(M, N), ws)
+
+
+def test_linear_lora_library_checks():
+    L = ivit.lib()
+
+    def call(M=32, K=64, N=48, n=3, R=16, rows=8, idx=P, ws=P, wb=32 * 16, gelu=False, rounding=0, out_bits=8, **ptr):
+        l = ivit.Lora(n, R, ptr.get("A", P), ptr.get("b_t", P), ptr.get("c_t", P), ptr.get("B", P))
+        lp = None if ptr.get("null") else C.byref(l)
+        if gelu:
+            return L.ivit_linear_lora_shiftgelu(P, M, K, P, N, None, P, P, rounding, lp, idx, rows, 4, 30, 8, D, P, ws, wb,
+                                                None)
+        return L.ivit_linear_lora(P, M, K, P, N, None, P, P, out_bits, rounding, lp, idx, rows, None, NONE, P, ws, wb,
+                                  None)
+
+    assert ivit.ivit_linear_lora_workspace_bytes(32, 16) == 512
+    assert ivit.ivit_linear_lora_workspace_bytes(33, 16) == 768
+    assert ivit.ivit_linear_lora_workspace_bytes(-1, 16) == 0
+    for gelu in (False, True):
+        for bad in (dict(R=8), dict(R=24), dict(R=144, wb=1 << 20), dict(n=0), dict(rows=0), dict(rows=5), dict(idx=None),
+                    dict(ws=None), dict(ws=P + 16), dict(wb=511), dict(A=None), dict(b_t=None), dict(c_t=None),
+                    dict(B=None), dict(A=P + 1), dict(B=P + 8), dict(idx=P + 4), dict(null=True), dict(rounding=2),
+                    dict(K=72), dict(N=40), dict(M=0)):
+            assert call(gelu=gelu, **bad) == 1, bad
+    assert call(out_bits=9) == 1
+    assert call(K=16400) == 2
+    assert L.ivit_linear_lora_shiftgelu(P, 32, 64, P, 48, None, P, P, 0, C.byref(ivit.Lora(3, 16, P, P, P, P)), P, 8, 0, 30,
+                                        8, D, P, P, 512, None) == 1
+
+
+def test_residual_norm_sizes():
+    r, c = 12, 64
+    n = (i8(c), i32(c), 7, 23, (1, 0))
+
+    def call(x=i8(r, c), o=i8(r, c), s=i32(c), y=i8(r, c), **k):
+        return (ivit.ivit_residual_norm, x, o, s, 1, 0, y), k
+
+    def run(check, **k):
+        a, kk = call(**k)
+        check(*a, **kk)
+
+    run(past_checks)
+    run(past_checks, post=n, pre=n, z=i8(r, c), gate=i8(3, c), gate_rows=5)
+    for bad in (dict(o=i8(r - 1, c)), dict(s=i32(c - 1)), dict(y=i8(r, c - 16)), dict(pre=n), dict(z=i8(r, c)),
+                dict(pre=n, z=i8(r, c + 16)), dict(gate=i8(2, c), gate_rows=5), dict(gate=i8(3, c), gate_rows=0),
+                dict(post=(i8(c - 1), i32(c), 7, 23, (1, 0))), dict(pre=(i8(c), i32(c + 1), 7, 23, (1, 0)), z=i8(r, c))):
+        run(refused, **bad)
+
+
+def test_residual_norm_library_checks():
+    L = ivit.lib()
+    X, O, G, Y, Z, S = (P + i * 0x10000 for i in range(6))
+
+    def call(skip=X, branch=O, rows=4, cols=32, post=True, gate=G, T=2, scale=S, b=1, c=0, pre=True, y=Y, z=Z, **n):
+        nm = ivit.Norm(n.get("gamma", P), n.get("beta", P), n.get("F", 7), n.get("M", 23), n.get("out", D))
+        p = C.byref(nm)
+        return L.ivit_residual_norm(skip, branch, rows, cols, p if post else None, gate, T, scale, b, c,
+                                    p if pre else None, y, z, None)
+
+    for bad in (dict(cols=24), dict(cols=0), dict(cols=2064), dict(rows=-1), dict(b=-1), dict(c=32), dict(c=-1),
+                dict(T=0), dict(skip=None), dict(branch=None), dict(scale=None), dict(y=None), dict(z=None),
+                dict(skip=X + 1), dict(branch=O + 8), dict(scale=S + 4), dict(y=Y + 2), dict(z=Z + 4), dict(gate=G + 1),
+                dict(gamma=None), dict(beta=None), dict(gamma=P + 1), dict(F=15), dict(F=-1), dict(M=24), dict(M=6),
+                dict(out=ivit.Dyadic(1, 32)), dict(out=ivit.Dyadic(-1, 3)),
+                # overlaps other than an output in an input's exact place
+                dict(y=X + 32), dict(z=O + 16), dict(y=G), dict(z=G + 32), dict(y=Z), dict(y=Z + 64), dict(y=X - 112)):
+        assert call(**bad) == 1, bad
+    assert call(rows=0, skip=None, branch=None, y=None, z=None, scale=None) == 0
+    assert call(rows=0, c=40) == 1
