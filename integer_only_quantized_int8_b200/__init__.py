@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 
 import torch
@@ -174,14 +175,13 @@ def lib() -> C.CDLL:
             L.ivit_linear_lora_workspace_bytes.restype = C.c_size_t
             L.ivit_linear_lora_workspace_bytes.argtypes = [i64, i32]
             L.ivit_linear_lora.restype = C.c_int
-            L.ivit_linear_lora.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, i32, i32, C.POINTER(Lora), vp, i64, vp,
+            L.ivit_linear_lora.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, i32, i32, vp, vp, i64, vp,
                                            Residual, vp, vp, C.c_size_t, vp]
             L.ivit_linear_lora_shiftgelu.restype = C.c_int
-            L.ivit_linear_lora_shiftgelu.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, i32, C.POINTER(Lora), vp, i64,
+            L.ivit_linear_lora_shiftgelu.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, i32, vp, vp, i64,
                                                      i32, i32, i32, Dyadic, vp, vp, C.c_size_t, vp]
             L.ivit_residual_norm.restype = C.c_int
-            L.ivit_residual_norm.argtypes = [vp, vp, i64, i32, C.POINTER(Norm), vp, i64, vp, i32, i32,
-                                             C.POINTER(Norm), vp, vp, vp]
+            L.ivit_residual_norm.argtypes = [vp, vp, i64, i32, vp, vp, i64, vp, i32, i32, vp, vp, vp, vp]
             L.ivit_selftest_withhold.restype = C.c_int
             L.ivit_selftest_withhold.argtypes = [i32, i32]
             L.ivit_selftest_int_rate.restype = C.c_int
@@ -225,13 +225,31 @@ def _holds(n: int, **tensors):
             raise ValueError(f"{name} holds {t.numel()} elements, needs {n}")
 
 
-def _here(t, dtype, name):
-    """_ptr of a tensor that must also live on the current device, where the
-    call's kernels and (without an explicit one) its stream are."""
+# The serving operators' calls are short enough for the time spent here to
+# count, so their wrappers take each tensor through one test of everything at
+# once, compare sizes in place, and pass small structures packed as bytes.
+
+def _at(t, dtype, dev, name):
+    """The device pointer of a tensor of the call, on the current device ``dev``; None stays None."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     p = _ptr(t, dtype, name)
-    if t is not None and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
     return p
+
+
+def _device(t, name) -> int:
+    """The current device, which the call's kernels and (without an explicit one) its stream are on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _dy(d) -> Dyadic:
@@ -376,24 +394,32 @@ def ivit_linear_lora_workspace_bytes(M: int, R: int) -> int:
     return int(lib().ivit_linear_lora_workspace_bytes(int(M), int(R)))
 
 
+_pack_lora = struct.Struct("@iiPPPP").pack         # ivit_lora
+_pack_norm = struct.Struct("@PPiiii").pack         # ivit_norm
+_NO_RESIDUAL = Residual(0, 0, 0)
+
+
 def _lora_args(X, W, bias, b, c, adapters, idx, rows, Y, skip=None):
-    """Shape checks shared by the linear layers with adapters; (M, K, N, Lora, idx pointer)."""
+    """Shape checks shared by the linear layers with adapters: (device, M, K, N, packed ivit_lora)."""
     M, K = X.shape
-    N = W.shape[0]
+    N, Kw = W.shape
     A, b_t, c_t, B = adapters
-    n, R = A.shape[0], A.shape[1]
-    if W.shape[1] != K or tuple(Y.shape) != (M, N) or tuple(A.shape) != (n, R, K) or tuple(B.shape) != (n, N, R):
+    n, R = A.shape[:2]
+    if Kw != K or Y.shape != (M, N) or A.shape != (n, R, K) or B.shape != (n, N, R):
         raise ValueError("shape mismatch")
-    if skip is not None and tuple(skip.shape) != (M, N):
+    if skip is not None and skip.shape != (M, N):
         raise ValueError("skip shape mismatch")
     if rows < 1 or M % rows:
         raise ValueError(f"shape mismatch: {M} rows are not requests of {rows}")
-    _holds(N, bias=bias, b=b, c=c)
-    _holds(n * R, b_t=b_t, c_t=c_t)
-    _holds(M // rows, idx=idx)
-    lora = Lora(n, R, _here(A, torch.int8, "A"), _here(b_t, torch.int32, "b_t"), _here(c_t, torch.int8, "c_t"),
-                _here(B, torch.int8, "B"))
-    return M, K, N, lora, _here(idx, torch.int32, "idx")
+    if b.numel() < N or c.numel() < N or (bias is not None and bias.numel() < N):
+        _holds(N, bias=bias, b=b, c=c)
+    if b_t.numel() < n * R or c_t.numel() < n * R:
+        _holds(n * R, b_t=b_t, c_t=c_t)
+    if idx.numel() < M // rows:
+        _holds(M // rows, idx=idx)
+    dev = _device(X, "X")
+    return dev, M, K, N, _pack_lora(n, R, _at(A, torch.int8, dev, "A"), _at(b_t, torch.int32, dev, "b_t"),
+                                    _at(c_t, torch.int8, dev, "c_t"), _at(B, torch.int8, dev, "B"))
 
 
 def ivit_linear_lora(X, W, bias, b, c, adapters, idx, rows: int, Y, workspace, out_bits: int = 8, skip=None, res=None,
@@ -401,37 +427,41 @@ def ivit_linear_lora(X, W, bias, b, c, adapters, idx, rows: int, Y, workspace, o
     """ivit_linear_requant with a low-rank adapter per request: rows [q * rows, (q + 1) * rows) of X take adapter
     idx[q] of ``adapters`` = (A [n,R,K] int8, b_t [n,R] int32, c_t [n,R] int8, B [n,N,R] int8), or none where idx[q]
     is outside [0, n)."""
-    M, K, N, lora, pidx = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y, skip)
-    st = lib().ivit_linear_lora(_here(X, torch.int8, "X"), M, K, _here(W, torch.int8, "W"), N,
-                                _here(bias, torch.int32, "bias"), _here(b, torch.int32, "b"), _here(c, torch.int8, "c"),
-                                int(out_bits), int(rounding), C.byref(lora), pidx, int(rows),
-                                _here(skip, torch.int8, "skip"), _res(res), _here(Y, torch.int8, "Y"),
-                                _here(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
-    _check("ivit_linear_lora", st)
+    dev, M, K, N, lora = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y, skip)
+    i8, i32 = torch.int8, torch.int32
+    st = (_lib or lib()).ivit_linear_lora(
+        _at(X, i8, dev, "X"), M, K, _at(W, i8, dev, "W"), N, None if bias is None else _at(bias, i32, dev, "bias"),
+        _at(b, i32, dev, "b"), _at(c, i8, dev, "c"), out_bits, rounding, lora, _at(idx, i32, dev, "idx"), rows,
+        None if skip is None else _at(skip, i8, dev, "skip"), _NO_RESIDUAL if res is None else _res(res),
+        _at(Y, i8, dev, "Y"), _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(),
+        _raw_stream(stream, dev))
+    if st:
+        _check("ivit_linear_lora", st)
     return Y
 
 
 def ivit_linear_lora_shiftgelu(X, W, bias, b, c, adapters, idx, rows: int, gelu_I0: int, gelu_M: int, gelu_k_out: int,
                                gelu_out, Y, workspace, stream=None, rounding: int = 0):
     """ivit_linear_shiftgelu with an adapter per request, as ivit_linear_lora."""
-    M, K, N, lora, pidx = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y)
-    st = lib().ivit_linear_lora_shiftgelu(_here(X, torch.int8, "X"), M, K, _here(W, torch.int8, "W"), N,
-                                          _here(bias, torch.int32, "bias"), _here(b, torch.int32, "b"),
-                                          _here(c, torch.int8, "c"), int(rounding), C.byref(lora), pidx, int(rows),
-                                          int(gelu_I0), int(gelu_M), int(gelu_k_out), _dy(gelu_out),
-                                          _here(Y, torch.int8, "Y"), _here(workspace, torch.uint8, "workspace"),
-                                          workspace.numel(), _stream(stream))
-    _check("ivit_linear_lora_shiftgelu", st)
+    dev, M, K, N, lora = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y)
+    i8, i32 = torch.int8, torch.int32
+    st = (_lib or lib()).ivit_linear_lora_shiftgelu(
+        _at(X, i8, dev, "X"), M, K, _at(W, i8, dev, "W"), N, None if bias is None else _at(bias, i32, dev, "bias"),
+        _at(b, i32, dev, "b"), _at(c, i8, dev, "c"), rounding, lora, _at(idx, i32, dev, "idx"), rows, gelu_I0, gelu_M,
+        gelu_k_out, _dy(gelu_out), _at(Y, i8, dev, "Y"), _at(workspace, torch.uint8, dev, "workspace"),
+        workspace.numel(), _raw_stream(stream, dev))
+    if st:
+        _check("ivit_linear_lora_shiftgelu", st)
     return Y
 
 
-def _norm(n, name):
-    """A ctypes Norm from (gamma, beta, F, M_ln, out), or None."""
+def _norm(n, dev, name):
+    """ivit_norm packed from (gamma, beta, F, M_ln, out), or None."""
     if n is None:
         return None
     gamma, beta, F, M_ln, out = n
-    return C.byref(Norm(_here(gamma, torch.int8, f"{name} gamma"), _here(beta, torch.int32, f"{name} beta"), int(F),
-                        int(M_ln), _dy(out)))
+    b, c = (out.b, out.c) if isinstance(out, Dyadic) else out
+    return _pack_norm(_at(gamma, torch.int8, dev, name), _at(beta, torch.int32, dev, name), F, M_ln, b, c)
 
 
 def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, gate=None, gate_rows: int = 1, pre=None,
@@ -440,23 +470,27 @@ def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, g
     its I-LayerNorm ``post`` and times its request's row of ``gate``, and z = I-LayerNorm ``pre`` of y.  skip, branch,
     y, z [rows, cols] int8; post and pre (gamma, beta, F, M_ln, out) or None; gate [ceil(rows / gate_rows), cols] int8
     or None; scale [cols] int32.  Returns (y, z)."""
-    rows, cols = skip.shape
-    if tuple(branch.shape) != (rows, cols) or tuple(y.shape) != (rows, cols) or scale.numel() != cols:
+    shape = skip.shape
+    rows, cols = shape
+    if branch.shape != shape or y.shape != shape or scale.numel() != cols:
         raise ValueError("shape mismatch")
-    if (pre is None) != (z is None) or (z is not None and tuple(z.shape) != (rows, cols)):
+    if (pre is None) != (z is None) or (z is not None and z.shape != shape):
         raise ValueError("z shape mismatch: z goes with pre")
-    if gate is not None:
-        if gate_rows < 1:
-            raise ValueError("shape mismatch: gate_rows < 1")
-        _holds(-(-rows // gate_rows) * cols, gate=gate)
-    for name, n in (("post", post), ("pre", pre)):
-        if n is not None and (n[0].numel() != cols or n[1].numel() != cols):
-            raise ValueError(f"{name} shape mismatch")
-    st = lib().ivit_residual_norm(_here(skip, torch.int8, "skip"), _here(branch, torch.int8, "branch"), rows, cols,
-                                  _norm(post, "post"), _here(gate, torch.int8, "gate"), int(gate_rows),
-                                  _here(scale, torch.int32, "scale"), int(b_skip), int(c), _norm(pre, "pre"),
-                                  _here(y, torch.int8, "y"), _here(z, torch.int8, "z"), _stream(stream))
-    _check("ivit_residual_norm", st)
+    if gate is not None and (gate_rows < 1 or gate.numel() < -(-rows // gate_rows) * cols):
+        raise ValueError(f"gate shape mismatch: one row of {cols} for every {gate_rows} rows")
+    if post is not None and (post[0].numel() != cols or post[1].numel() != cols):
+        raise ValueError("post shape mismatch")
+    if pre is not None and (pre[0].numel() != cols or pre[1].numel() != cols):
+        raise ValueError("pre shape mismatch")
+    dev = _device(skip, "skip")
+    i8 = torch.int8
+    st = (_lib or lib()).ivit_residual_norm(
+        _at(skip, i8, dev, "skip"), _at(branch, i8, dev, "branch"), rows, cols, _norm(post, dev, "post"),
+        None if gate is None else _at(gate, i8, dev, "gate"), gate_rows, _at(scale, torch.int32, dev, "scale"), b_skip, c,
+        _norm(pre, dev, "pre"), _at(y, i8, dev, "y"), None if z is None else _at(z, i8, dev, "z"),
+        _raw_stream(stream, dev))
+    if st:
+        _check("ivit_residual_norm", st)
     return y, z
 
 
