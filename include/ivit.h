@@ -221,7 +221,8 @@ ivit_status ivit_layernorm_ptf(const int8_t *x, int64_t rows, int32_t cols, cons
 
 /* ---------------------------------------------------------------------------
  * One shared model serving many requests: low-rank adapters, gated and scaled
- * residual branches.  The pages have no counterpart; READING: each is put in the integer form of the operators above (int8
+ * residual branches, differential attention.  The pages have no counterpart;
+ * READING: each is put in the integer form of the operators above (int8
  * tensors, dyadic requant with floor shifts, 32-bit accumulators).
  * ------------------------------------------------------------------------- */
 
@@ -293,6 +294,24 @@ ivit_status ivit_residual_norm(const int8_t *skip, const int8_t *branch, int64_t
                                const ivit_norm *post, const int8_t *gate, int64_t gate_rows, const int32_t *scale,
                                int32_t b_skip, int32_t c, const ivit_norm *pre, int8_t *y, int8_t *z,
                                ivit_stream_t stream);
+
+/* Differential attention: head h of H has two query/key pairs of width 64 and
+ * one value of width 128, and attends with the difference of two Shiftmax
+ * maps, the second weighted by lambda_h:
+ *   L^m    = logits of (Q^m, K^m) as in ivit_attention, e^m = ShiftExp(L^m - max L^m)
+ *   P^1_ij = (floor(2^M / sum_j e^1) * e^1_ij) >> (M - (k_out - 1))
+ *   P^2_ij = (floor(lam_h / sum_j e^2) * e^2_ij) >> (M - (k_out - 1))
+ *   ctx_id = sat_8((out.b * sum_j (P^1_ij - P^2_ij) V_jd) >> out.c)
+ * The weight rides on IntDiv's numerator: lam_h = round(lambda_h 2^M), so both
+ * maps are 8-bit integers of one scale and their difference is exact.
+ * qkv [B*N x 3*D] int8, D = 128 * H: columns [0, D) are Q (Q^1 of head h at
+ * 128 h, Q^2 at 128 h + 64), [D, 2D) K likewise, [2D, 3D) V (head h at 128 h).
+ * lam [H] int32 (device), clamped to [0, 2^M].  ctx [B*N x D] int8.
+ * Constraints: B, N >= 0, H >= 1; N <= 640; 2 <= k_s <= 8; I0 >= 1;
+ * k_out - 1 <= M <= 30; 1 <= k_out <= 8.                                    */
+ivit_status ivit_attention_diff(const int8_t *qkv, int32_t B, int32_t N, int32_t H, ivit_dyadic logit, int32_t k_s,
+                                int32_t I0, int32_t M, int32_t k_out, const int32_t *lam, ivit_dyadic out,
+                                int8_t *ctx, ivit_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * The encoder block ([IVIT] 3.1): X^ = MSA(LN1(X)) + X; Y = MLP(LN2(X^)) + X^

@@ -27,7 +27,7 @@ __all__ = [
     "ivit_model_workspace_bytes", "ivit_model_forward", "ivit_selftest_wait_timeout", "ivit_selftest_int_rate",
     "ivit_shiftgelu_rowmax", "ivit_attention_lis", "ivit_layernorm_ptf", "ivit_selftest_withhold",
     "Lora", "Norm", "ivit_linear_lora_workspace_bytes", "ivit_linear_lora", "ivit_linear_lora_shiftgelu",
-    "ivit_residual_norm",
+    "ivit_residual_norm", "ivit_attention_diff",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +46,7 @@ EXPORTED_SYMBOLS = (
     "ivit_selftest_wait_timeout", "ivit_selftest_int_rate",
     "ivit_shiftgelu_rowmax", "ivit_attention_lis", "ivit_layernorm_ptf", "ivit_selftest_withhold",
     "ivit_linear_lora_workspace_bytes", "ivit_linear_lora", "ivit_linear_lora_shiftgelu", "ivit_residual_norm",
+    "ivit_attention_diff",
 )
 
 _STATUS = {0: "IVIT_OK", 1: "IVIT_ERR_INVALID_ARG", 2: "IVIT_ERR_UNSUPPORTED", 3: "IVIT_ERR_CUDA",
@@ -182,6 +183,8 @@ def lib() -> C.CDLL:
                                                      i32, i32, i32, Dyadic, vp, vp, C.c_size_t, vp]
             L.ivit_residual_norm.restype = C.c_int
             L.ivit_residual_norm.argtypes = [vp, vp, i64, i32, vp, vp, i64, vp, i32, i32, vp, vp, vp, vp]
+            L.ivit_attention_diff.restype = C.c_int
+            L.ivit_attention_diff.argtypes = [vp, i32, i32, i32, Dyadic, i32, i32, i32, i32, vp, Dyadic, vp, vp]
             L.ivit_selftest_withhold.restype = C.c_int
             L.ivit_selftest_withhold.argtypes = [i32, i32]
             L.ivit_selftest_int_rate.restype = C.c_int
@@ -492,6 +495,23 @@ def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, g
     if st:
         _check("ivit_residual_norm", st)
     return y, z
+
+
+def ivit_attention_diff(qkv, B: int, N: int, H: int, logit, k_s: int, I0: int, M: int, k_out: int, lam, out, ctx,
+                        stream=None):
+    """ctx [B*N, 128*H] from qkv [B*N, 3*128*H]: each head attends with the difference of two Shiftmax maps, the second
+    weighted by lam[h] / 2^M (lam [H] int32)."""
+    if qkv.shape != (B * N, 384 * H) or ctx.shape != (B * N, 128 * H):
+        raise ValueError("shape mismatch")
+    if lam.numel() < H:
+        _holds(H, lam=lam)
+    dev = _device(qkv, "qkv")
+    st = (_lib or lib()).ivit_attention_diff(
+        _at(qkv, torch.int8, dev, "qkv"), B, N, H, _dy(logit), k_s, I0, M, k_out, _at(lam, torch.int32, dev, "lam"),
+        _dy(out), _at(ctx, torch.int8, dev, "ctx"), _raw_stream(stream, dev))
+    if st:
+        _check("ivit_attention_diff", st)
+    return ctx
 
 
 def ivit_block_workspace_bytes(B: int, N: int, D: int, Dm: int) -> int:

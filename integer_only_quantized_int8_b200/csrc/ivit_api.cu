@@ -430,6 +430,21 @@ ivit_status ivit_residual_norm(const int8_t* skip, const int8_t* branch, int64_t
                               (cudaStream_t)stream);
 }
 
+ivit_status ivit_attention_diff(const int8_t* qkv, int32_t B, int32_t N, int32_t H, ivit_dyadic logit, int32_t k_s,
+                                int32_t I0, int32_t M, int32_t k_out, const int32_t* lam, ivit_dyadic out,
+                                int8_t* ctx, ivit_stream_t stream) {
+  if (B < 0 || N < 0 || H < 1 || k_s < 2 || k_s > 8 || !valid_shiftmax(I0, M, k_out) || !valid_dyadic(logit) ||
+      !valid_dyadic(out))
+    return IVIT_ERR_INVALID_ARG;
+  if (N > 640 || (int64_t)B * N > 0x7fffff00LL || H > 2048) return IVIT_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0) return IVIT_OK;
+  if (!qkv || !ctx || !lam || !aligned16(qkv) || !aligned16(ctx) || !aligned16(lam)) return IVIT_ERR_INVALID_ARG;
+  DeviceCtx dc;
+  const ivit_status st = device_ctx(&dc);
+  if (st != IVIT_OK) return st;
+  return launch_attention_diff(dc, qkv, B, N, H, logit, k_s, I0, M, k_out, lam, out, ctx, (cudaStream_t)stream);
+}
+
 size_t ivit_block_workspace_bytes(int32_t B, int32_t N, int32_t D, int32_t Dm) {
   if (B < 0 || N < 0 || D < 0 || Dm < 0) return 0;
   const size_t T = (size_t)B * (size_t)N;

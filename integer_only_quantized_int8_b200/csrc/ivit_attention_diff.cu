@@ -1,0 +1,612 @@
+// ivit_attention_diff.cu -- differential attention on sm_100a (ivit_attention_diff):
+// per head two query/key pairs of width 64, one value of width 128, and
+//   ctx = sat_8((b_o sum_j (P1 - P2)_ij V_j) >> c_o),
+// P1 and P2 the integer Shiftmax maps of the two pairs, P2's IntDiv numerator
+// carrying the weight lambda_h 2^M.
+//
+// One CTA per SM walks work items (tile of query rows, head, image).  Both maps
+// of an item are worked on at once, each by a softmax group of eight warps:
+//   warp 0       TMA producer: Q and K of both pairs (one ring), V (another);
+//   warps 1, 2   S issuer of map 0 / 1: S = Q K^T in chunks of keys into the
+//                map's TMEM score buffer;
+//   warp 3       P V issuer: O = P1 V, then O += (-P2) V onto the same
+//                accumulator: P1 <= 128 is a u8 operand, -P2 >= -128 an s8 one,
+//                so the difference needs no ninth bit and V is read as it is;
+//   warps 4-19   two softmax groups;
+//   warps 20-23  output readout of the previous item, one per TMEM lane quarter.
+//
+// Shiftmax needs a row's maximum before any exponential and its sum before any
+// probability, so a row is passed over three times:
+//   pass 1  reads each score once from TMEM, keeps the raw maximum (the logit
+//           requant is monotone) and writes the saturated 8-bit logits back to
+//           TMEM, four to a column -- a quarter of the score's space, which
+//           frees the score buffer for the next chunk at once and makes 640
+//           keys of two maps fit;
+//   pass 2  looks e = ShiftExp(L - max L) up and sums it;
+//   pass 3  looks e up again and writes P in the logits' place, which is also
+//           the layout in which the P V MMA takes its A operand from TMEM
+//           (lane = row, four 8-bit values of K per column): P never passes
+//           through shared memory.
+// The table address of a score is one dp4a: byte * (-128) + (base + 128 max L),
+// the table being replicated once per shared-memory bank (row stride 128 bytes,
+// lane l reads copy l: no conflicts).  The four warps of a lane quarter's rows
+// (w, w + 4 of each group) split a row's keys; partial maxima and sums meet in
+// shared memory.
+//
+// Keys past the last one are masked where they lie: out of the maximum and the
+// sum, and to P = 0.  Whatever their logit bytes hold, their table addresses stay
+// inside shared memory (|max L - L| <= 255 entries of 128 bytes, and the table
+// lies above 64 KB of operands).
+#include <climits>
+
+#include "ivit_common.cuh"
+#include "ivit_internal.h"
+
+namespace ivit {
+namespace {
+
+constexpr int kHeadDim = 64;   // width of one query / key of a pair
+constexpr int kValDim = 128;   // width of a value
+constexpr int kQTile = 128;    // TMEM lanes; a tile holds up to this many query rows
+constexpr int kMaxKeys = 640;
+constexpr int kSoftWarps = 8;  // per map
+constexpr int kSoftBase = 4, kReadBase = kSoftBase + 2 * kSoftWarps;
+constexpr int kDiffThreads = 32 * (kReadBase + 4);
+
+struct DiffArgs {
+  int32_t B, N, H;
+  int32_t qrows;  // query rows per tile: 128, 64 or 32
+  int32_t logit_b, logit_c, bq;
+  int32_t k_s, ks_lo, ks_hi;
+  int32_t I0, M, k_out;
+  const int32_t* lam;
+  int32_t out_b, out_c, out_bq, out_fast, o_lo, o_hi;
+  int8_t* ctx;
+  int* status;
+};
+
+struct DiffLayout {
+  int n64, n32, n16;
+  int chunk, nchunks;          // keys per score chunk (a multiple of 16), chunks
+  int lcols;                   // TMEM columns of one map's logits / P
+  int sep;                     // O has columns of its own (else the score buffers')
+  int o_col, s_col, s_stride;  // first columns of O and of map 0's score buffer
+  int qk_bytes, v_bytes, depth;
+  int v_off, tab_off, part_off, bar_off, total;
+};
+
+__host__ __device__ inline DiffLayout diff_layout(int N) {
+  DiffLayout L;
+  L.n64 = (N + 63) / 64 * 64;
+  L.n32 = (N + 31) / 32 * 32;
+  L.n16 = (N + 15) / 16 * 16;
+  L.lcols = (L.n32 / 4 + 31) / 32 * 32;
+  // 512 columns: both maps' logits, O, and the two score buffers of at least 96
+  L.sep = 2 * L.lcols + kValDim + 2 * 96 <= 512;
+  const int avail = (512 - 2 * L.lcols - (L.sep ? kValDim : 0)) / 2 / 32 * 32;
+  const int widest = avail < 256 ? avail : 256;
+  L.nchunks = (L.n16 + widest - 1) / widest;
+  L.chunk = ((L.n16 + L.nchunks - 1) / L.nchunks + 15) / 16 * 16;
+  L.o_col = 2 * L.lcols;
+  L.s_col = 2 * L.lcols + (L.sep ? kValDim : 0);
+  L.s_stride = avail;
+  L.qk_bytes = 2 * (kQTile + L.n64) * kHeadDim;
+  L.v_bytes = L.n64 * kValDim;
+  const int rest = 256 * 128 + 2 * 2 * 2 * kQTile * 4 + 256;
+  L.depth = 2 * (L.qk_bytes + L.v_bytes) + rest + 1024 <= 227 * 1024 ? 2 : 1;
+  L.v_off = L.depth * L.qk_bytes;
+  L.tab_off = L.v_off + L.depth * L.v_bytes;
+  L.part_off = L.tab_off + 256 * 128;
+  L.bar_off = L.part_off + 2 * 2 * 2 * kQTile * 4;  // [map][max, sum][half][row]
+  L.total = L.bar_off + 256;
+  return L;
+}
+
+IVIT_DEV uint32_t pack_sat4_diff(int32_t y0, int32_t y1, int32_t y2, int32_t y3) {
+  uint32_t t, d;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(t) : "r"(y3), "r"(y2), "r"(0u));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(y1), "r"(y0), "r"(t));
+  return d;
+}
+
+// floor(b S / 2^c) before the saturation: one mul.hi when bq = b 2^(32 - c) fits a positive int32
+template <bool FASTQ>
+IVIT_DEV int32_t logit_of(int32_t S, const DiffArgs& a) {
+  if (FASTQ) return __mulhi(a.bq, S);
+  const int64_t q = ((int64_t)a.logit_b * (int64_t)S) >> a.logit_c;
+  return (int32_t)(q < (int64_t)INT_MIN ? (int64_t)INT_MIN : (q > (int64_t)INT_MAX ? (int64_t)INT_MAX : q));
+}
+
+// bounded wait that also gives up at once when another thread has
+IVIT_DEV bool diff_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag) {
+  if (*abort_flag) return false;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitBudgetNs) {
+      report_timeout(status);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+IVIT_DEV void group_bar(int g) { asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(32 * kSoftWarps) : "memory"); }
+
+IVIT_DEV void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+IVIT_DEV void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+IVIT_DEV void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+IVIT_DEV void tmem_ld8_wait(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], kind::i8, int32 accumulate; single thread.
+IVIT_DEV void umma_i8_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+IVIT_DEV int32_t lds32(uint32_t addr) {
+  int32_t v;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// exponentials of the four logits of w; base = table + 4 lane + 128 max L
+IVIT_DEV void exp4(uint32_t w, int32_t base, uint32_t (&e)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e[i] = (uint32_t)lds32((uint32_t)__dp4a((int)w, (int)(0x80u << (8 * i)), base));
+}
+
+template <bool FASTQ>
+__global__ void __launch_bounds__(kDiffThreads, 1)
+    attention_diff_kernel(const __grid_constant__ CUtensorMap tm, const DiffArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  const int N = a.N;
+  const DiffLayout L = diff_layout(N);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bar_off);
+  uint64_t* qk_full = bars + 0;    // [2] Q and K of both pairs landed
+  uint64_t* qk_empty = bars + 2;   // [2] both maps' scores computed (one commit per S issuer)
+  uint64_t* v_full = bars + 4;     // [2]
+  uint64_t* v_empty = bars + 6;    // [2] P V of the item done
+  uint64_t* s_full = bars + 8;     // [2] a score chunk of map g
+  uint64_t* s_empty = bars + 10;   // [2] read by the group's warps
+  uint64_t* p_full = bars + 12;    // [2] P of map g in TMEM
+  uint64_t* p_empty = bars + 14;   // [2] consumed by P V
+  uint64_t* o_full = bars + 16;
+  uint64_t* o_empty = bars + 17;   // read out (one arrival per readout warp)
+  uint64_t* drain = bars + 18;     // every MMA of the CTA done (one commit per issuer)
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 19);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 20);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qtiles = (N + a.qrows - 1) / a.qrows;
+  const int n_items = qtiles * a.H * a.B;
+  const int n_local = n_items > (int)blockIdx.x ? (n_items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  const int D = a.H * kValDim;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qk_full[i], 1);
+      mbar_init(&qk_empty[i], 2);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], kSoftWarps);
+      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&p_empty[i], 1);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, 4);
+    mbar_init(drain, 3);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm);
+  }
+  if (warp == 3) {
+    __syncwarp();
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  // tab[t * 32 + l] = ShiftExp(-t) for every lane l: one evaluation per entry,
+  // staged in the partials' space
+  int32_t* stage_t = reinterpret_cast<int32_t*>(smem + L.part_off);
+  if (tid < 256) stage_t[tid] = tid < (1 << a.k_s) ? shift_exp(-tid, a.I0) : 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  for (int i4 = tid; i4 < 256 * 8; i4 += kDiffThreads) {
+    const int32_t e = stage_t[i4 >> 3];
+    reinterpret_cast<int4*>(smem + L.tab_off)[i4] = make_int4(e, e, e, e);
+  }
+  __syncthreads();
+  const uint32_t tmem = *tslot;
+  pdl_wait();  // qkv comes from the previous kernel
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      for (int j = 0; j < n_local; ++j) {
+        const int s = j % L.depth;
+        const uint32_t ph = (uint32_t)((j / L.depth) & 1);
+        const int item = (int)blockIdx.x + j * (int)gridDim.x;
+        const int qt = item % qtiles, h = (item / qtiles) % a.H, img = item / (qtiles * a.H);
+        const int row0 = img * N;
+        if (!diff_wait(&qk_empty[s], ph ^ 1, a.status, abort_flag)) break;
+        uint8_t* st = smem + s * L.qk_bytes;
+        mbar_arrive_expect_tx(&qk_full[s], (uint32_t)L.qk_bytes);
+        for (int m = 0; m < 2; ++m) {
+          uint8_t* q = st + m * (kQTile + L.n64) * kHeadDim;
+          const int col = h * kValDim + m * kHeadDim;
+          for (int i = 0; i < 2; ++i)
+            tma_load_2d(q + i * 64 * kHeadDim, &tm, col, row0 + qt * a.qrows + 64 * i, &qk_full[s]);
+          for (int i = 0; i < L.n64 / 64; ++i)
+            tma_load_2d(q + (kQTile + 64 * i) * kHeadDim, &tm, D + col, row0 + 64 * i, &qk_full[s]);
+        }
+        if (!diff_wait(&v_empty[s], ph ^ 1, a.status, abort_flag)) break;
+        uint8_t* v = smem + L.v_off + s * L.v_bytes;  // two 64-wide halves
+        mbar_arrive_expect_tx(&v_full[s], (uint32_t)L.v_bytes);
+        for (int m = 0; m < 2; ++m)
+          for (int i = 0; i < L.n64 / 64; ++i)
+            tma_load_2d(v + (m * L.n64 + 64 * i) * kHeadDim, &tm, 2 * D + h * kValDim + m * kHeadDim, row0 + 64 * i,
+                        &v_full[s]);
+      }
+    }
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ S issuer of map g
+    if (lane == 0) {
+      const int g = warp - 1;
+      const uint32_t d_s = tmem + (uint32_t)(L.s_col + g * L.s_stride);
+      uint32_t n = 0;  // chunks issued
+      bool ok = true;
+      for (int j = 0; j < n_local && ok; ++j) {
+        const int s = j % L.depth;
+        if (!diff_wait(&qk_full[s], (uint32_t)((j / L.depth) & 1), a.status, abort_flag)) break;
+        // O of the previous item lies in the score buffers
+        if (!L.sep && j > 0 && !diff_wait(o_empty, (uint32_t)((j - 1) & 1), a.status, abort_flag)) break;
+        const uint32_t qa = smem_u32(smem + s * L.qk_bytes + g * (kQTile + L.n64) * kHeadDim);
+        const uint32_t ka = qa + kQTile * kHeadDim;
+        for (int c = 0; c < L.nchunks; ++c, ++n) {
+          if (!diff_wait(&s_empty[g], (n & 1) ^ 1, a.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int w = min(L.chunk, L.n16 - c * L.chunk);
+          const uint32_t idesc = idesc_i8(kQTile, w, true, true, false);
+          const uint32_t kc = ka + (uint32_t)(c * L.chunk * kHeadDim);
+#pragma unroll
+          for (int k = 0; k < kHeadDim / 32; ++k)
+            umma_i8(d_s, smem_desc(qa + k * 32, 16, 512, kSwizzle64B), smem_desc(kc + k * 32, 16, 512, kSwizzle64B),
+                    idesc, k != 0);
+          umma_commit(&s_full[g]);
+        }
+        umma_commit(&qk_empty[s]);
+      }
+      umma_commit(drain);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ P V issuer
+    if (lane == 0) {
+      const uint32_t d_o = tmem + (uint32_t)L.o_col;
+      bool ok = true;
+      for (int j = 0; j < n_local && ok; ++j) {
+        const int s = j % L.depth;
+        const uint32_t ph = (uint32_t)(j & 1);
+        ok = diff_wait(&v_full[s], (uint32_t)((j / L.depth) & 1), a.status, abort_flag) &&
+             diff_wait(&p_full[0], ph, a.status, abort_flag);
+        // O's columns: read out (own region), or no longer holding either map's scores
+        if (ok) ok = L.sep ? (j == 0 || diff_wait(o_empty, ph ^ 1, a.status, abort_flag))
+                           : diff_wait(&p_full[1], ph, a.status, abort_flag);
+        for (int g = 0; g < 2 && ok; ++g) {
+          if (g == 1 && L.sep) ok = diff_wait(&p_full[1], ph, a.status, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t idesc = idesc_i8(kQTile, kHeadDim, g == 1, true, true);
+          const uint32_t pa = tmem + (uint32_t)(g * L.lcols);
+          const uint32_t va = smem_u32(smem + L.v_off + s * L.v_bytes);
+          for (int k = 0; k < L.n32 / 32; ++k)
+            for (int m = 0; m < 2; ++m)
+              umma_i8_ta(d_o + (uint32_t)(m * kHeadDim), pa + (uint32_t)(8 * k),
+                         smem_desc(va + (uint32_t)((m * L.n64 + 32 * k) * kHeadDim), 512, 512, kSwizzle64B), idesc,
+                         (uint32_t)(g | k));
+          umma_commit(&p_empty[g]);
+        }
+        if (!ok) break;
+        umma_commit(&v_empty[s]);
+        umma_commit(o_full);
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, a.status);  // before TMEM is released
+    }
+  } else if (warp < kReadBase) {
+    // ------------------------------------------------------------ softmax group of map g
+    const int sw = warp - kSoftBase;
+    const int g = sw / kSoftWarps;
+    const int half = (sw >> 2) & 1;  // which half of the row's keys
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t t_s = t_lane + (uint32_t)(L.s_col + g * L.s_stride);
+    const uint32_t t_l = t_lane + (uint32_t)(g * L.lcols);
+    int32_t* part = reinterpret_cast<int32_t*>(smem + L.part_off) + g * (4 * kQTile);  // [max, sum][half][row]
+    const uint32_t tab = smem_u32(smem + L.tab_off) + (uint32_t)(4 * lane);
+    // passes 2 and 3: this half's 32-key units (8 logit columns each)
+    const int units = L.n32 / 32;
+    const int u_lo = half ? (units + 1) / 2 : 0, u_hi = half ? units : (units + 1) / 2;
+    const int pshift = a.M - (a.k_out - 1);
+    uint32_t n = 0;  // chunks seen
+    bool ok = true;
+    for (int j = 0; j < n_local; ++j) {
+      const int item = (int)blockIdx.x + j * (int)gridDim.x;
+      const int qt = item % qtiles, h = (item / qtiles) % a.H;
+      // warps whose rows all lie past the tile or the image's last token skip the passes
+      const bool rows = quarter * 32 < min(a.qrows, N - qt * a.qrows);
+
+      uint32_t num = 1u << a.M;  // IntDiv's numerator
+      if (g == 1) num = (uint32_t)min(max(__ldg(a.lam + h), 0), 1 << a.M);
+
+      // ---- pass 1: maximum of the raw scores, 8-bit logits into TMEM
+      int32_t mx = INT_MIN;
+      if (j > 0) {  // the previous item's P has been consumed
+        if (ok) ok = diff_wait(&p_empty[g], (uint32_t)((j - 1) & 1), a.status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      for (int c = 0; c < L.nchunks; ++c, ++n) {
+        if (ok) ok = diff_wait(&s_full[g], n & 1, a.status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const int k0 = c * L.chunk;
+        const int w = min(L.chunk, L.n16 - k0);
+        if (ok && rows) {
+          // the halves take alternate 16-key units
+          for (int u = half; u < w / 16; u += 2) {
+            uint32_t r[16];
+            tmem_ld16(t_s + (uint32_t)(16 * u), r);
+            tmem_ld_wait_regs(r);
+            const int key = k0 + 16 * u, lim = N - key;
+            if (lim >= 16) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) mx = max(mx, (int32_t)r[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i < lim) mx = max(mx, (int32_t)r[i]);
+            }
+            uint32_t lw[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              int32_t l[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                l[i] = logit_of<FASTQ>((int32_t)r[4 * q + i], a);
+                if (a.k_s < 8) l[i] = min(max(l[i], a.ks_lo), a.ks_hi);
+              }
+              lw[q] = pack_sat4_diff(l[0], l[1], l[2], l[3]);
+            }
+            tmem_st4(t_l + (uint32_t)(key / 4), lw[0], lw[1], lw[2], lw[3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[g]);
+      }
+      tmem_st_wait();
+      part[half * kQTile + row] = mx;
+      tc_fence_before();
+      group_bar(g);
+      tc_fence_after();
+      const int32_t smax = max(part[row], part[kQTile + row]);
+      const int32_t lmax = min(max(logit_of<FASTQ>(smax, a), a.ks_lo), a.ks_hi);
+      const int32_t base = (int32_t)tab + 128 * lmax;
+
+      // ---- pass 2: row sum of the exponentials
+      uint32_t sum = 0;
+      if (ok && rows) {
+        for (int u = u_lo; u < u_hi; ++u) {
+          uint32_t r[8];
+          tmem_ld8(t_l + (uint32_t)(8 * u), r);
+          tmem_ld8_wait(r);
+          const int lim = N - 32 * u;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t e[4];
+            exp4(r[q], base, e);
+            if (lim >= 32) {
+              sum += (e[0] + e[1]) + (e[2] + e[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum += 4 * q + i < lim ? e[i] : 0u;
+            }
+          }
+        }
+      }
+      part[(2 + half) * kQTile + row] = (int32_t)sum;
+      group_bar(g);
+      sum = (uint32_t)part[2 * kQTile + row] + (uint32_t)part[3 * kQTile + row];
+      if (sum == 0) sum = 1;  // rows that skipped the passes
+      const uint32_t dv = num / sum;
+
+      // ---- pass 3: P = (Dv e) >> (M - k_out + 1) in the logits' place
+      if (ok && rows) {
+        // (Dv e) >> pshift is one mul.hi by Dv 2^(32 - pshift) when Dv < 2^pshift
+        const bool hip = pshift >= 1 && __all_sync(0xffffffffu, (uint64_t)dv < ((uint64_t)1 << pshift));
+        const uint32_t dvh = hip ? dv << (32 - pshift) : 0u;
+        for (int u = u_lo; u < u_hi; ++u) {
+          uint32_t r[8];
+          tmem_ld8(t_l + (uint32_t)(8 * u), r);
+          tmem_ld8_wait(r);
+          const int lim = N - 32 * u;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t e[4];
+            exp4(r[q], base, e);
+            uint32_t w;
+            if (hip)
+              w = __umulhi(dvh, e[0]) + __umulhi(dvh, e[1]) * 256u + __umulhi(dvh, e[2]) * 65536u +
+                  __umulhi(dvh, e[3]) * 16777216u;
+            else
+              w = ((dv * e[0]) >> pshift) + ((dv * e[1]) >> pshift) * 256u + ((dv * e[2]) >> pshift) * 65536u +
+                  ((dv * e[3]) >> pshift) * 16777216u;
+            if (lim < 32) {
+              const int left = lim - 4 * q;  // keys of this word
+              w = left >= 4 ? w : (left <= 0 ? 0u : w & ((1u << (8 * left)) - 1u));
+            }
+            // bytes p <= 128: -p = (128 - p) ^ 128, without a borrow between bytes
+            r[q] = g == 0 ? w : (0x80808080u - w) ^ 0x80808080u;
+          }
+          tmem_st8(t_l + (uint32_t)(8 * u), r);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[g]);
+    }
+  } else {
+    // ------------------------------------------------------------ readout warps
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    bool ok = true;
+    for (int j = 0; j < n_local; ++j) {
+      const int item = (int)blockIdx.x + j * (int)gridDim.x;
+      const int qt = item % qtiles, h = (item / qtiles) % a.H, img = item / (qtiles * a.H);
+      if (ok) ok = diff_wait(o_full, (uint32_t)(j & 1), a.status, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      const int nrow = min(a.qrows, N - qt * a.qrows);  // rows of the tile
+      if (ok && quarter * 32 < nrow) {
+        const uint32_t t_o = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)L.o_col;
+        int8_t* dst = a.ctx + (int64_t)(img * N + qt * a.qrows + row) * D + h * kValDim;
+#pragma unroll
+        for (int pr = 0; pr < 4; ++pr) {
+          uint32_t ra[16], rb[16];
+          tmem_ld16(t_o + (uint32_t)(32 * pr), ra);
+          tmem_ld16(t_o + (uint32_t)(32 * pr + 16), rb);
+          tmem_ld_wait_regs2(ra, rb);
+          if (row < nrow) {
+            uint32_t packed[8];
+#pragma unroll
+            for (int wd = 0; wd < 8; ++wd) {
+              int32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int32_t acc = (int32_t)(wd < 4 ? ra[wd * 4 + e] : rb[(wd - 4) * 4 + e]);
+                if (a.out_fast) {
+                  y[e] = __mulhi(a.out_bq, acc);  // floor(b_o acc / 2^c_o), exact
+                } else {
+                  const int32_t ac = min(max(acc, a.o_lo), a.o_hi);
+                  const int64_t v = (int64_t)a.out_b * ac;  // |v >> c| < 2^31 after the clamp
+                  y[e] = (int32_t)__funnelshift_r((uint32_t)v, (uint32_t)(v >> 32), (uint32_t)a.out_c);
+                }
+              }
+              packed[wd] = pack_sat4_diff(y[0], y[1], y[2], y[3]);
+            }
+            reinterpret_cast<int4*>(dst + 32 * pr)[0] = make_int4(packed[0], packed[1], packed[2], packed[3]);
+            reinterpret_cast<int4*>(dst + 32 * pr)[1] = make_int4(packed[4], packed[5], packed[6], packed[7]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_t B, int32_t N, int32_t H,
+                                  ivit_dyadic logit, int32_t k_s, int32_t I0, int32_t M, int32_t k_out,
+                                  const int32_t* lam, ivit_dyadic out, int8_t* ctx, cudaStream_t stream) {
+  const int64_t T = (int64_t)B * N;
+  const uint64_t width = (uint64_t)3 * kValDim * (uint64_t)H;
+  CUtensorMap tm;
+  const ivit_status st = encode_tmap_2d_u8(&tm, qkv, width, (uint64_t)T, width, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != IVIT_OK) return st;
+  DiffArgs a{};
+  a.B = B;
+  a.N = N;
+  a.H = H;
+  a.qrows = kQTile;
+  const bool fastq = logit.c >= 1 && (int64_t)logit.b < ((int64_t)1 << (logit.c - 1));
+  a.logit_b = logit.b;
+  a.logit_c = logit.c;
+  a.bq = fastq ? (int32_t)((int64_t)logit.b << (32 - logit.c)) : 0;
+  a.k_s = k_s;
+  a.ks_lo = -(1 << (k_s - 1));
+  a.ks_hi = (1 << (k_s - 1)) - 1;
+  a.I0 = I0;
+  a.M = M;
+  a.k_out = k_out;
+  a.lam = lam;
+  a.out_b = out.b;
+  a.out_c = out.c;
+  a.out_fast = out.c >= 1 && (int64_t)out.b < ((int64_t)1 << (out.c - 1));
+  a.out_bq = a.out_fast ? (int32_t)((int64_t)out.b << (32 - out.c)) : 0;
+  // acc in [-u, u], u = 128 / 2^s with 2^s <= b / 2^c < 2^(s+1), keeps every unsaturated result,
+  // saturates the rest the same way and keeps (b acc) >> c within int32
+  a.o_lo = INT_MIN;
+  a.o_hi = INT_MAX;
+  if (out.b != 0) {
+    int bl = 0;
+    while (bl < 31 && (out.b >> bl) != 0) ++bl;
+    const int sh = bl - 1 - out.c;
+    const int64_t u = sh >= 7 ? 1 : (sh >= 0 ? (128 >> sh) : ((int64_t)128 << (-sh)));
+    a.o_hi = (int32_t)(u > INT_MAX ? INT_MAX : u);
+    a.o_lo = -a.o_hi;
+  }
+  a.ctx = ctx;
+  a.status = dc.status;
+  const int64_t items = (int64_t)((N + a.qrows - 1) / a.qrows) * H * B;
+  if (items > 0x7fffffff) return IVIT_ERR_UNSUPPORTED;
+  const int smem = diff_layout(N).total + 1024;
+  auto kern = fastq ? attention_diff_kernel<true> : attention_diff_kernel<false>;
+  static bool attr_done[64];  // per device; benign race: the attribute value is the same
+  if (!attr_done[dc.device]) {
+    if (cudaFuncSetAttribute(attention_diff_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(attention_diff_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+            cudaSuccess)
+      return IVIT_ERR_CUDA;
+    attr_done[dc.device] = true;
+  }
+  const unsigned grid = (unsigned)(items < dc.num_sms ? items : dc.num_sms);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kDiffThreads), (size_t)smem, stream, tm, a);
+  note_launch();
+  return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
+}
+
+}  // namespace ivit

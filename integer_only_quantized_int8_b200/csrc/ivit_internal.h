@@ -130,6 +130,11 @@ ivit_status launch_residual_norm(const DeviceCtx& dc, const int8_t* skip, const 
                                  const int32_t* scale, int32_t b_skip, int32_t c, const ivit_norm* pre, int8_t* y,
                                  int8_t* z, cudaStream_t stream);
 
+// Differential attention (H pairs of 64-wide maps; see ivit_attention_diff).
+ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_t B, int32_t N, int32_t H,
+                                  ivit_dyadic logit, int32_t k_s, int32_t I0, int32_t M, int32_t k_out,
+                                  const int32_t* lam, ivit_dyadic out, int8_t* ctx, cudaStream_t stream);
+
 ivit_status launch_layernorm(const DeviceCtx& dc, const int8_t* x, int64_t rows, int32_t cols,
                              const int8_t* gamma, const int32_t* beta, int32_t F, int32_t M_ln, ivit_dyadic out,
                              int8_t* y, cudaStream_t stream);

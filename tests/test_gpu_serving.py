@@ -1,6 +1,7 @@
 """GPU parity of the serving operators against their plain 64-bit forms, bit
 for bit (every quantity is an integer): linear layers with a low-rank adapter
-per request, the end of a residual branch.  Outputs sit between canary bytes."""
+per request, the end of a residual branch, differential attention, and a block
+of all three.  Outputs sit between canary bytes."""
 import numpy as np
 import pytest
 import torch
@@ -276,3 +277,155 @@ def test_residual_norm_capture_and_empty():
     np.testing.assert_array_equal(host(y), want[0])
     np.testing.assert_array_equal(host(z), want[1])
     ivit.ivit_residual_norm(dx[:0], do[:0], ds, 1, 0, y[:0], pre=dp, z=z[:0])
+
+
+# ---------------------------------------------------------------- differential attention
+
+DIFF_ARGS = ((1 << 20, 28), 8, 20, 30, 8)   # logits of std ~56 at |q|, |k| ~ 30
+
+
+def diff_inputs(B, N, H, seed, spread=30):
+    r = np.random.default_rng(seed)
+    qkv = np.clip(np.round(r.standard_normal((B * N, 384 * H)) * spread), -128, 127).astype(np.int8)
+    return qkv, r.integers(0, (1 << 30) + 1, H).astype(np.int32)
+
+
+def diff_check(qkv, B, N, H, args, lam, out):
+    ctx, untouched = guarded((B * N, 128 * H))
+    ivit.ivit_attention_diff(dev(qkv), B, N, H, *args, dev(lam), out, ctx)
+    np.testing.assert_array_equal(host(ctx), serving.attention_diff(qkv, B, N, H, *args, lam, out))
+    assert untouched()
+
+
+@pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 96, 97, 112, 127, 128, 129, 144, 160, 161, 192, 193,
+                               197, 224, 225, 255, 256, 257, 288, 320, 321, 383, 384, 385, 448, 449, 511, 512, 513, 576, 577,
+                               608, 609, 639, 640])
+def test_attention_diff_parity(N):
+    qkv, lam = diff_inputs(2, N, 2, seed=N)
+    diff_check(qkv, 2, N, 2, DIFF_ARGS, lam, (1 << 20, 25))
+
+
+@pytest.mark.parametrize("B,N,H", [(1, 197, 3), (40, 197, 6), (9, 130, 9), (200, 5, 3), (6, 577, 6), (33, 64, 5), (3, 260, 20)])
+def test_attention_diff_many_items(B, N, H):
+    """More work items than SMs: every ring and phase wraps."""
+    qkv, lam = diff_inputs(B, N, H, seed=B + N)
+    diff_check(qkv, B, N, H, DIFF_ARGS, lam, (1 << 20, 25))
+
+
+@pytest.mark.parametrize("k_s,I0,M,k_out", [(8, 1, 30, 8), (2, 3, 30, 8), (4, 5, 12, 4), (6, 97, 7, 8), (8, 1 << 22, 30, 8),
+                                            (8, 20, 30, 1), (8, 20, 0, 1), (3, 1000, 30, 8), (8, 7, 20, 6)])
+@pytest.mark.parametrize("N", [37, 197, 470])
+def test_attention_diff_constants(k_s, I0, M, k_out, N):
+    qkv, _ = diff_inputs(2, N, 2, seed=k_s)
+    lam = np.array([(1 << M) // 3, 1 << M], np.int32)
+    diff_check(qkv, 2, N, 2, ((1 << 20, 26), k_s, I0, M, k_out), lam, (3, 2))
+
+
+@pytest.mark.parametrize("logit", [(0, 5), (1, 0), ((1 << 31) - 1, 0), ((1 << 31) - 1, 31), (3, 1), (1 << 30, 31), (1, 31)])
+@pytest.mark.parametrize("out", [(0, 0), (1, 0), ((1 << 31) - 1, 0), (7, 4), ((1 << 31) - 1, 31)])
+def test_attention_diff_multipliers_of_every_size(logit, out):
+    qkv, lam = diff_inputs(2, 70, 2, seed=3, spread=80)
+    diff_check(qkv, 2, 70, 2, (logit, 8, 20, 30, 8), lam, out)
+
+
+@pytest.mark.parametrize("lam", [[0, 0], [1 << 30, 1 << 30], [-5, (1 << 31) - 1], [-(1 << 31), 1]])
+def test_attention_diff_weights(lam):
+    """lam is clamped to [0, 2^M]; 0 leaves the first map alone."""
+    qkv, _ = diff_inputs(2, 150, 2, seed=4)
+    diff_check(qkv, 2, 150, 2, DIFF_ARGS, np.array(lam, np.int32), (1 << 20, 25))
+
+
+@pytest.mark.parametrize("N", [40, 200, 600])
+def test_attention_diff_extreme_values(N):
+    """Every product of one sign; one key that takes a whole row; keys of the next image that would win every maximum."""
+    qkv, lam = diff_inputs(2, N, 1, seed=5)
+    qkv[:] = -128
+    diff_check(qkv, 2, N, 1, ((1, 0), 8, 1, 30, 8), lam, (1, 7))
+    qkv, _ = diff_inputs(2, N, 1, seed=6)
+    qkv[N - 1, 128:256] = 127
+    qkv[:, :128] = np.abs(qkv[:, :128].astype(np.int32)).clip(0, 127)
+    qkv[N:, 128:256] = 127
+    diff_check(qkv, 2, N, 1, DIFF_ARGS, lam, (1 << 20, 25))
+
+
+def test_attention_diff_capture_streams_and_empty():
+    qkv, lam = diff_inputs(8, 197, 3, seed=7)
+    other, _ = diff_inputs(8, 197, 3, seed=8)
+    out = (1 << 20, 25)
+    want = [serving.attention_diff(t, 8, 197, 3, *DIFF_ARGS, lam, out) for t in (qkv, other)]
+    d, dl = [dev(qkv), dev(other)], dev(lam)
+    ctx = [torch.empty(8 * 197, 384, dtype=torch.int8, device="cuda") for _ in d]
+    streams = [torch.cuda.Stream() for _ in d]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            ivit.ivit_attention_diff(d[i], 8, 197, 3, *DIFF_ARGS, dl, out, ctx[i], stream=s)
+    for c, w in zip(ctx, want):
+        np.testing.assert_array_equal(host(c), w)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ivit.ivit_attention_diff(d[0], 8, 197, 3, *DIFF_ARGS, dl, out, ctx[0])
+    d[0].copy_(d[1])
+    for _ in range(2):
+        ctx[0].zero_()
+        g.replay()
+        np.testing.assert_array_equal(host(ctx[0]), want[1])
+    ivit.ivit_attention_diff(d[0][:0], 0, 197, 3, *DIFF_ARGS, dl, out, ctx[0][:0])
+
+
+# ---------------------------------------------------------------- together
+
+def test_adapted_block():
+    """An encoder block of these operators alone, as a server runs it: adapters on all four linear layers, differential
+    attention between them, the branch ends with post-norm, gate, residual scale and the next norm; then once more
+    from a graph on other inputs."""
+    B, N, H = 5, 197, 2
+    Dm, D = 512, 128 * H
+    r = np.random.default_rng(9)
+    layers = [LoraCase(B, N, K, n, 16, 3, seed=s, idx=[0, -1, 2, 1, 0])
+              for s, (K, n) in enumerate([(D, 3 * D), (D, D), (D, Dm), (Dm, D)], 20)]
+    pre, post, nxt = (norm_params(r, D) for _ in range(3))
+    gate, lam = rng_i8(r, B, D), r.integers(0, 1 << 30, H).astype(np.int32)
+    scale = (r.standard_normal(D) * 4e6).astype(np.int32)
+    out = (1 << 20, 25)
+
+    def host_block(x, z):
+        def lin(i, t, gelu=None):
+            q = layers[i]
+            return serving.linear_lora(t, q.W, q.bias, q.b, q.c, q.adapters, q.idx, N, gelu=gelu)
+        ctx = serving.attention_diff(lin(0, z), B, N, H, *DIFF_ARGS, lam, out)
+        x, z = serving.residual_norm(x, lin(1, ctx), scale, 939524096, 30, post, gate, N, pre)
+        return serving.residual_norm(x, lin(3, lin(2, z, GELU)), scale, 939524096, 30, post, gate, N, nxt)
+
+    d = [q.device() for q in layers]
+    dpre, dpost, dnxt = dev_norm(pre), dev_norm(post), dev_norm(nxt)
+    dg, dl, ds = dev(gate), dev(lam), dev(scale)
+    buf = [torch.empty(B * N, w, dtype=torch.int8, device="cuda") for w in (3 * D, D, D, Dm, D)]
+    x, z = rng_i8(r, B * N, D), rng_i8(r, B * N, D)
+    dx, dz, ws = dev(x), dev(z), workspace(B * N, 16)
+
+    def block():
+        ivit.ivit_linear_lora(dz, *d[0][1:], buf[0], ws)
+        ivit.ivit_attention_diff(buf[0], B, N, H, *DIFF_ARGS, dl, out, buf[1])
+        ivit.ivit_linear_lora(buf[1], *d[1][1:], buf[2], ws)
+        ivit.ivit_residual_norm(dx, buf[2], ds, 939524096, 30, dx, dpost, dg, N, dpre, dz)
+        ivit.ivit_linear_lora_shiftgelu(dz, *d[2][1:], *GELU, buf[3], ws)
+        ivit.ivit_linear_lora(buf[3], *d[3][1:], buf[4], ws)
+        ivit.ivit_residual_norm(dx, buf[4], ds, 939524096, 30, dx, dpost, dg, N, dnxt, dz)
+
+    for _ in range(3):    # the block's outputs are its next inputs
+        block()
+        x, z = host_block(x, z)
+    np.testing.assert_array_equal(host(dx), x)
+    np.testing.assert_array_equal(host(dz), z)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        block()
+    x, z = rng_i8(r, B * N, D), rng_i8(r, B * N, D)
+    dx.copy_(dev(x))
+    dz.copy_(dev(z))
+    for _ in range(2):
+        g.replay()
+        x, z = host_block(x, z)
+    np.testing.assert_array_equal(host(dx), x)
+    np.testing.assert_array_equal(host(dz), z)

@@ -123,3 +123,23 @@ def test_residual_norm_library_checks():
         assert call(**bad) == 1, bad
     assert call(rows=0, skip=None, branch=None, y=None, z=None, scale=None) == 0
     assert call(rows=0, c=40) == 1
+
+
+def test_attention_diff_checks():
+    args = ((1, 0), 8, 4, 30, 8)
+    past_checks(ivit.ivit_attention_diff, i8(18, 768), 2, 9, 2, *args, i32(2), (1, 0), i8(18, 256))
+    for qkv, lam, ctx in ((i8(18, 384), i32(2), i8(18, 256)), (i8(17, 768), i32(2), i8(18, 256)),
+                          (i8(18, 768), i32(1), i8(18, 256)), (i8(18, 768), i32(2), i8(18, 128))):
+        refused(ivit.ivit_attention_diff, qkv, 2, 9, 2, *args, lam, (1, 0), ctx)
+    L = ivit.lib()
+
+    def call(qkv=P, B=2, N=9, H=2, logit=D, k_s=8, I0=4, M=30, k_out=8, lam=P, out=D, ctx=P):
+        return L.ivit_attention_diff(qkv, B, N, H, logit, k_s, I0, M, k_out, lam, out, ctx, None)
+
+    for bad in (dict(qkv=None), dict(lam=None), dict(ctx=None), dict(qkv=P + 1), dict(lam=P + 4), dict(ctx=P + 8),
+                dict(B=-1), dict(N=-1), dict(H=0), dict(k_s=1), dict(k_s=9), dict(I0=0), dict(I0=(1 << 22) + 1), dict(M=31),
+                dict(M=6), dict(k_out=0), dict(k_out=9), dict(logit=ivit.Dyadic(1, 32)), dict(out=ivit.Dyadic(-1, 0))):
+        assert call(**bad) == 1, bad
+    assert call(N=641) == 2
+    assert call(H=2049) == 2
+    assert call(B=0) == 0 and call(N=0) == 0
