@@ -53,18 +53,6 @@ constexpr int kSoftWarps = 8;  // per map
 constexpr int kSoftBase = 4, kReadBase = kSoftBase + 2 * kSoftWarps;
 constexpr int kDiffThreads = 32 * (kReadBase + 4);
 
-struct DiffArgs {
-  int32_t B, N, H;
-  int32_t qrows;  // query rows per tile: 128, 64 or 32
-  int32_t logit_b, logit_c, bq;
-  int32_t k_s, ks_lo, ks_hi;
-  int32_t I0, M, k_out;
-  const int32_t* lam;
-  int32_t out_b, out_c, out_bq, out_fast, o_lo, o_hi;
-  int8_t* ctx;
-  int* status;
-};
-
 struct DiffLayout {
   int n64, n32, n16;
   int chunk, nchunks;          // keys per score chunk (a multiple of 16), chunks
@@ -75,7 +63,7 @@ struct DiffLayout {
   int v_off, tab_off, part_off, bar_off, total;
 };
 
-__host__ __device__ inline DiffLayout diff_layout(int N) {
+inline DiffLayout diff_layout(int N) {
   DiffLayout L;
   L.n64 = (N + 63) / 64 * 64;
   L.n32 = (N + 31) / 32 * 32;
@@ -101,6 +89,19 @@ __host__ __device__ inline DiffLayout diff_layout(int N) {
   L.total = L.bar_off + 256;
   return L;
 }
+
+struct DiffArgs {
+  int32_t B, N, H;
+  int32_t qrows;  // query rows per tile: 128, 64 or 32
+  int32_t logit_b, logit_c, bq;
+  int32_t k_s, ks_lo, ks_hi;
+  int32_t I0, M, k_out;
+  const int32_t* lam;
+  int32_t out_b, out_c, out_bq, out_fast, o_lo, o_hi;
+  DiffLayout L;
+  int8_t* ctx;
+  int* status;
+};
 
 IVIT_DEV uint32_t pack_sat4_diff(int32_t y0, int32_t y1, int32_t y2, int32_t y3) {
   uint32_t t, d;
@@ -133,7 +134,8 @@ IVIT_DEV bool diff_wait(uint64_t* bar, uint32_t parity, int* status, volatile in
   }
 }
 
-IVIT_DEV void group_bar(int g) { asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(32 * kSoftWarps) : "memory"); }
+// named barrier of the two warps that share a map's 32 rows (ids 1..8)
+IVIT_DEV void pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(1 + id) : "memory"); }
 
 IVIT_DEV void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
@@ -174,19 +176,115 @@ IVIT_DEV int32_t lds32(uint32_t addr) {
   return v;
 }
 
+// Streams units 0..n-1 of kCols TMEM columns through body(r, u), the next
+// unit's load in flight while one is worked on.
+IVIT_DEV void unit_ld(uint32_t t, uint32_t (&r)[8]) { tmem_ld8(t, r); }
+IVIT_DEV void unit_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
+IVIT_DEV void unit_wait(uint32_t (&r)[8]) { tmem_ld8_wait(r); }
+IVIT_DEV void unit_wait(uint32_t (&r)[16]) { tmem_ld_wait_regs(r); }
+template <int kCols, typename F>
+IVIT_DEV void stream_units(uint32_t t, int step, int n, F&& body) {
+  uint32_t a[kCols];
+#pragma unroll 1
+  for (int u = 0; u < n; ++u) {
+    unit_ld(t + (uint32_t)(u * step), a);
+    unit_wait(a);
+    body(a, u);
+  }
+}
+
 // exponentials of the four logits of w; base = table + 4 lane + 128 max L
 IVIT_DEV void exp4(uint32_t w, int32_t base, uint32_t (&e)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) e[i] = (uint32_t)lds32((uint32_t)__dp4a((int)w, (int)(0x80u << (8 * i)), base));
 }
 
-template <bool FASTQ>
+// the low (TOP: top) bytes of four words
+template <bool TOP>
+IVIT_DEV uint32_t bytes4(uint32_t e0, uint32_t e1, uint32_t e2, uint32_t e3) {
+  constexpr uint32_t sel = TOP ? 0x0073u : 0x0040u;
+  return __byte_perm(__byte_perm(e0, e1, sel), __byte_perm(e2, e3, sel), 0x5410u);
+}
+
+// the first n bytes of a word (n <= 0: none, n >= 4: all)
+IVIT_DEV uint32_t first_bytes(uint32_t w, int n) { return n >= 4 ? w : (n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u)); }
+
+// Pass 1 of one 16-key unit: the raw maximum, and the saturated logits as four words.
+template <bool FASTQ, bool NARROW, bool RAGGED>
+IVIT_DEV void logits16(const uint32_t (&r)[16], int lim, const DiffArgs& a, int32_t& mx, uint32_t (&lw)[4]) {
+  int32_t m0 = mx, m1 = INT_MIN;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    m0 = __vimax3_s32(m0, RAGGED && i >= lim ? INT_MIN : (int32_t)r[i], RAGGED && i + 1 >= lim ? INT_MIN : (int32_t)r[i + 1]);
+    m1 = __vimax3_s32(m1, RAGGED && i + 2 >= lim ? INT_MIN : (int32_t)r[i + 2],
+                      RAGGED && i + 3 >= lim ? INT_MIN : (int32_t)r[i + 3]);
+  }
+  mx = max(m0, m1);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    int32_t l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      l[i] = logit_of<FASTQ>((int32_t)r[4 * q + i], a);
+      if (NARROW) l[i] = min(max(l[i], a.ks_lo), a.ks_hi);
+    }
+    lw[q] = pack_sat4_diff(l[0], l[1], l[2], l[3]);
+  }
+}
+
+// Pass 2 of one 32-key unit: the exponentials' sum; E8 leaves them in r, a byte each.
+template <bool E8, bool RAGGED>
+IVIT_DEV void sum32(uint32_t (&r)[8], int lim, int32_t base, uint32_t& sum) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t e[4];
+    exp4(r[q], base, e);
+    if (E8) {
+      uint32_t w = bytes4<false>(e[0], e[1], e[2], e[3]);
+      if (RAGGED) w = first_bytes(w, lim - 4 * q);
+      r[q] = w;
+      sum = __dp4a(w, 0x01010101u, sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += RAGGED && 4 * q + i >= lim ? 0u : e[i];
+    }
+  }
+}
+
+// Pass 3 of one 32-key unit: r becomes P (or, neg, -P) bytes.  dvs e carries
+// P = (Dv e) >> pshift in its top byte; SHR: only after a further shift by rsh.
+template <bool E8, bool SHR, bool RAGGED>
+IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t dvs, int rsh, bool neg) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t e[4];
+    if (E8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = __byte_perm(r[q], 0u, 0x4440u + i);
+    } else {
+      exp4(r[q], base, e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[i] *= dvs;
+      if (SHR) e[i] >>= rsh;
+    }
+    uint32_t w = bytes4<true>(e[0], e[1], e[2], e[3]);
+    if (RAGGED && !E8) w = first_bytes(w, lim - 4 * q);
+    // bytes p <= 128: -p = (128 - p) ^ 128, without a borrow between bytes
+    r[q] = neg ? (0x80808080u - w) ^ 0x80808080u : w;
+  }
+}
+
+// FASTQ: the logit requant is one mul.hi.  NARROW: k_s < 8, so the saturation is
+// not the byte pack's.  E8: every exponential fits a byte (I0 <= 255).
+template <bool FASTQ, bool NARROW, bool E8>
 __global__ void __launch_bounds__(kDiffThreads, 1)
-    attention_diff_kernel(const __grid_constant__ CUtensorMap tm, const DiffArgs a) {
+    attention_diff_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ DiffArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   const int N = a.N;
-  const DiffLayout L = diff_layout(N);
+  const DiffLayout& L = a.L;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bar_off);
   uint64_t* qk_full = bars + 0;    // [2] Q and K of both pairs landed
   uint64_t* qk_empty = bars + 2;   // [2] both maps' scores computed (one commit per S issuer)
@@ -349,16 +447,23 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     const int g = sw / kSoftWarps;
     const int half = (sw >> 2) & 1;  // which half of the row's keys
     const int quarter = warp & 3;
+    const int pair = 4 * g + quarter;
     const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t t_s = t_lane + (uint32_t)(L.s_col + g * L.s_stride);
     const uint32_t t_l = t_lane + (uint32_t)(g * L.lcols);
     int32_t* part = reinterpret_cast<int32_t*>(smem + L.part_off) + g * (4 * kQTile);  // [max, sum][half][row]
     const uint32_t tab = smem_u32(smem + L.tab_off) + (uint32_t)(4 * lane);
-    // passes 2 and 3: this half's 32-key units (8 logit columns each)
+    // passes 2 and 3: this half's 32-key units (8 logit columns each); the last unit of
+    // all is ragged when it holds keys past N
     const int units = L.n32 / 32;
-    const int u_lo = half ? (units + 1) / 2 : 0, u_hi = half ? units : (units + 1) / 2;
+    const int u_lo = half ? (units + 1) / 2 : 0, u_n = (half ? units : (units + 1) / 2) - u_lo;
+    const int u_ragged = (N & 31) != 0 && u_lo + u_n == units && u_n > 0 ? u_n - 1 : -1;
+    const int lim_ragged = N - 32 * (units - 1);
+    const uint32_t t_u = t_l + (uint32_t)(8 * u_lo);
+    // P = (Dv e) >> pshift in the top byte of (Dv << lsh) e >> rsh: |.| <= 2^(23 + k_out) <= 2^31
     const int pshift = a.M - (a.k_out - 1);
+    const int lsh = max(24 - pshift, 0), rsh = max(pshift - 24, 0);
     uint32_t n = 0;  // chunks seen
     bool ok = true;
     for (int j = 0; j < n_local; ++j) {
@@ -366,7 +471,6 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       const int qt = item % qtiles, h = (item / qtiles) % a.H;
       // warps whose rows all lie past the tile or the image's last token skip the passes
       const bool rows = quarter * 32 < min(a.qrows, N - qt * a.qrows);
-
       uint32_t num = 1u << a.M;  // IntDiv's numerator
       if (g == 1) num = (uint32_t)min(max(__ldg(a.lam + h), 0), 1 << a.M);
 
@@ -381,108 +485,66 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         const int k0 = c * L.chunk;
-        const int w = min(L.chunk, L.n16 - k0);
-        if (ok && rows) {
-          // the halves take alternate 16-key units
-          for (int u = half; u < w / 16; u += 2) {
-            uint32_t r[16];
-            tmem_ld16(t_s + (uint32_t)(16 * u), r);
-            tmem_ld_wait_regs(r);
-            const int key = k0 + 16 * u, lim = N - key;
-            if (lim >= 16) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) mx = max(mx, (int32_t)r[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (i < lim) mx = max(mx, (int32_t)r[i]);
-            }
+        const int nu = min(L.chunk, L.n16 - k0) / 16;  // 16-key units, taken by the halves in turn
+        if (ok && rows)
+          stream_units<16>(t_s + (uint32_t)(16 * half), 32, (nu - half + 1) / 2, [&](uint32_t(&r)[16], int u) {
+            const int key = k0 + 16 * half + 32 * u;
             uint32_t lw[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              int32_t l[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                l[i] = logit_of<FASTQ>((int32_t)r[4 * q + i], a);
-                if (a.k_s < 8) l[i] = min(max(l[i], a.ks_lo), a.ks_hi);
-              }
-              lw[q] = pack_sat4_diff(l[0], l[1], l[2], l[3]);
-            }
+            if (N - key >= 16)
+              logits16<FASTQ, NARROW, false>(r, 16, a, mx, lw);
+            else
+              logits16<FASTQ, NARROW, true>(r, N - key, a, mx, lw);
             tmem_st4(t_l + (uint32_t)(key / 4), lw[0], lw[1], lw[2], lw[3]);
-          }
-        }
+          });
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[g]);
       }
-      tmem_st_wait();
-      part[half * kQTile + row] = mx;
-      tc_fence_before();
-      group_bar(g);
-      tc_fence_after();
-      const int32_t smax = max(part[row], part[kQTile + row]);
-      const int32_t lmax = min(max(logit_of<FASTQ>(smax, a), a.ks_lo), a.ks_hi);
-      const int32_t base = (int32_t)tab + 128 * lmax;
+      if (rows) {
+        tmem_st_wait();
+        part[half * kQTile + row] = mx;
+        tc_fence_before();
+        pair_bar(pair);
+        tc_fence_after();
+        const int32_t smax = max(part[row], part[kQTile + row]);
+        const int32_t lmax = min(max(logit_of<FASTQ>(smax, a), a.ks_lo), a.ks_hi);
+        const int32_t base = (int32_t)tab + 128 * lmax;
 
-      // ---- pass 2: row sum of the exponentials
-      uint32_t sum = 0;
-      if (ok && rows) {
-        for (int u = u_lo; u < u_hi; ++u) {
-          uint32_t r[8];
-          tmem_ld8(t_l + (uint32_t)(8 * u), r);
-          tmem_ld8_wait(r);
-          const int lim = N - 32 * u;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint32_t e[4];
-            exp4(r[q], base, e);
-            if (lim >= 32) {
-              sum += (e[0] + e[1]) + (e[2] + e[3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) sum += 4 * q + i < lim ? e[i] : 0u;
-            }
-          }
-        }
-      }
-      part[(2 + half) * kQTile + row] = (int32_t)sum;
-      group_bar(g);
-      sum = (uint32_t)part[2 * kQTile + row] + (uint32_t)part[3 * kQTile + row];
-      if (sum == 0) sum = 1;  // rows that skipped the passes
-      const uint32_t dv = num / sum;
-
-      // ---- pass 3: P = (Dv e) >> (M - k_out + 1) in the logits' place
-      if (ok && rows) {
-        // (Dv e) >> pshift is one mul.hi by Dv 2^(32 - pshift) when Dv < 2^pshift
-        const bool hip = pshift >= 1 && __all_sync(0xffffffffu, (uint64_t)dv < ((uint64_t)1 << pshift));
-        const uint32_t dvh = hip ? dv << (32 - pshift) : 0u;
-        for (int u = u_lo; u < u_hi; ++u) {
-          uint32_t r[8];
-          tmem_ld8(t_l + (uint32_t)(8 * u), r);
-          tmem_ld8_wait(r);
-          const int lim = N - 32 * u;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint32_t e[4];
-            exp4(r[q], base, e);
-            uint32_t w;
-            if (hip)
-              w = __umulhi(dvh, e[0]) + __umulhi(dvh, e[1]) * 256u + __umulhi(dvh, e[2]) * 65536u +
-                  __umulhi(dvh, e[3]) * 16777216u;
+        // ---- pass 2: row sum of the exponentials
+        uint32_t sum = 0;
+        if (ok) {
+          stream_units<8>(t_u, 8, u_n, [&](uint32_t(&r)[8], int u) {
+            if (u != u_ragged)
+              sum32<E8, false>(r, 32, base, sum);
             else
-              w = ((dv * e[0]) >> pshift) + ((dv * e[1]) >> pshift) * 256u + ((dv * e[2]) >> pshift) * 65536u +
-                  ((dv * e[3]) >> pshift) * 16777216u;
-            if (lim < 32) {
-              const int left = lim - 4 * q;  // keys of this word
-              w = left >= 4 ? w : (left <= 0 ? 0u : w & ((1u << (8 * left)) - 1u));
-            }
-            // bytes p <= 128: -p = (128 - p) ^ 128, without a borrow between bytes
-            r[q] = g == 0 ? w : (0x80808080u - w) ^ 0x80808080u;
-          }
-          tmem_st8(t_l + (uint32_t)(8 * u), r);
+              sum32<E8, true>(r, lim_ragged, base, sum);
+            if (E8) tmem_st8(t_u + (uint32_t)(8 * u), r);
+          });
+          if (E8) tmem_st_wait();
         }
+        part[(2 + half) * kQTile + row] = (int32_t)sum;
+        pair_bar(pair);
+        sum = (uint32_t)part[2 * kQTile + row] + (uint32_t)part[3 * kQTile + row];
+        const uint32_t dvs = (num / max(sum, 1u)) << lsh;
+
+        // ---- pass 3: P in the logits' place
+        if (ok) {
+          if (rsh == 0)
+            stream_units<8>(t_u, 8, u_n, [&](uint32_t(&r)[8], int u) {
+              if (E8 || u != u_ragged)
+                prob32<E8, false, false>(r, 32, base, dvs, 0, g == 1);
+              else
+                prob32<E8, false, true>(r, lim_ragged, base, dvs, 0, g == 1);
+              tmem_st8(t_u + (uint32_t)(8 * u), r);
+            });
+          else
+            stream_units<8>(t_u, 8, u_n, [&](uint32_t(&r)[8], int u) {
+              prob32<E8, true, true>(r, u != u_ragged ? 32 : lim_ragged, base, dvs, rsh, g == 1);
+              tmem_st8(t_u + (uint32_t)(8 * u), r);
+            });
+        }
+        tmem_st_wait();
       }
-      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[g]);
@@ -592,15 +654,20 @@ ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_
   a.status = dc.status;
   const int64_t items = (int64_t)((N + a.qrows - 1) / a.qrows) * H * B;
   if (items > 0x7fffffff) return IVIT_ERR_UNSUPPORTED;
-  const int smem = diff_layout(N).total + 1024;
-  auto kern = fastq ? attention_diff_kernel<true> : attention_diff_kernel<false>;
+  a.L = diff_layout(N);
+  const int smem = a.L.total + 1024;
+  using Kernel = void (*)(CUtensorMap, DiffArgs);
+  static const Kernel kernels[8] = {
+      attention_diff_kernel<false, false, false>, attention_diff_kernel<false, false, true>,
+      attention_diff_kernel<false, true, false>,  attention_diff_kernel<false, true, true>,
+      attention_diff_kernel<true, false, false>,  attention_diff_kernel<true, false, true>,
+      attention_diff_kernel<true, true, false>,   attention_diff_kernel<true, true, true>};
+  const Kernel kern = kernels[(fastq ? 4 : 0) + (k_s < 8 ? 2 : 0) + (I0 <= 255 ? 1 : 0)];
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
-    if (cudaFuncSetAttribute(attention_diff_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(attention_diff_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-            cudaSuccess)
-      return IVIT_ERR_CUDA;
+    for (const Kernel k : kernels)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+        return IVIT_ERR_CUDA;
     attr_done[dc.device] = true;
   }
   const unsigned grid = (unsigned)(items < dc.num_sms ? items : dc.num_sms);
