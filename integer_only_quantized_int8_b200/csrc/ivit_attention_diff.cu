@@ -50,6 +50,8 @@ constexpr int kValDim = 128;   // width of a value
 constexpr int kQTile = 128;    // TMEM lanes; a tile holds up to this many query rows
 constexpr int kMaxKeys = 640;
 constexpr int kSoftWarps = 8;  // per map
+constexpr int kMaxChunk = 128;  // keys per score chunk
+constexpr int kChunkUnits = kMaxChunk / 32;  // 16-key units of a chunk per half
 constexpr int kSoftBase = 4, kReadBase = kSoftBase + 2 * kSoftWarps;
 constexpr int kDiffThreads = 32 * (kReadBase + 4);
 
@@ -72,7 +74,7 @@ inline DiffLayout diff_layout(int N) {
   // 512 columns: both maps' logits, O, and the two score buffers of at least 96
   L.sep = 2 * L.lcols + kValDim + 2 * 96 <= 512;
   const int avail = (512 - 2 * L.lcols - (L.sep ? kValDim : 0)) / 2 / 32 * 32;
-  const int widest = avail < 256 ? avail : 256;
+  const int widest = avail < kMaxChunk ? avail : kMaxChunk;
   L.nchunks = (L.n16 + widest - 1) / widest;
   L.chunk = ((L.n16 + L.nchunks - 1) / L.nchunks + 15) / 16 * 16;
   L.o_col = 2 * L.lcols;
@@ -251,10 +253,10 @@ IVIT_DEV void sum32(uint32_t (&r)[8], int lim, int32_t base, uint32_t& sum) {
   }
 }
 
-// Pass 3 of one 32-key unit: r becomes P (or, neg, -P) bytes.  dvs e carries
+// Pass 3 of one 32-key unit: r becomes P (neg = 127 in every byte: -P) bytes.  dvs e carries
 // P = (Dv e) >> pshift in its top byte; SHR: only after a further shift by rsh.
 template <bool E8, bool SHR, bool RAGGED>
-IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t dvs, int rsh, bool neg) {
+IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t dvs, int rsh, uint32_t neg) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     uint32_t e[4];
@@ -271,8 +273,40 @@ IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t dvs, int 
     }
     uint32_t w = bytes4<true>(e[0], e[1], e[2], e[3]);
     if (RAGGED && !E8) w = first_bytes(w, lim - 4 * q);
-    // bytes p <= 128: -p = (128 - p) ^ 128, without a borrow between bytes
-    r[q] = neg ? (0x80808080u - w) ^ 0x80808080u : w;
+    // -p of a byte p <= 128 is (p + 127) ^ 127, without a carry between bytes
+    r[q] = (w + neg) ^ neg;
+  }
+}
+
+// One row of O to 128 bytes of ctx: sat_8((b_o O) >> c_o).
+template <bool FAST>
+IVIT_DEV void read_out(uint32_t t_o, bool live, int8_t* dst, const DiffArgs& a) {
+#pragma unroll 1
+  for (int pr = 0; pr < 4; ++pr) {
+    uint32_t ra[16], rb[16];
+    tmem_ld16(t_o + (uint32_t)(32 * pr), ra);
+    tmem_ld16(t_o + (uint32_t)(32 * pr + 16), rb);
+    tmem_ld_wait_regs2(ra, rb);
+    uint32_t packed[8];
+#pragma unroll
+    for (int wd = 0; wd < 8; ++wd) {
+      int32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int32_t acc = (int32_t)(wd < 4 ? ra[wd * 4 + e] : rb[(wd - 4) * 4 + e]);
+        if (FAST) {
+          y[e] = __mulhi(a.out_bq, acc);  // floor(b_o acc / 2^c_o), exact
+        } else {
+          const int64_t v = (int64_t)a.out_b * min(max(acc, a.o_lo), a.o_hi);  // |v >> c| < 2^31 after the clamp
+          y[e] = (int32_t)__funnelshift_r((uint32_t)v, (uint32_t)(v >> 32), (uint32_t)a.out_c);
+        }
+      }
+      packed[wd] = pack_sat4_diff(y[0], y[1], y[2], y[3]);
+    }
+    if (live) {
+      reinterpret_cast<int4*>(dst + 32 * pr)[0] = make_int4(packed[0], packed[1], packed[2], packed[3]);
+      reinterpret_cast<int4*>(dst + 32 * pr)[1] = make_int4(packed[4], packed[5], packed[6], packed[7]);
+    }
   }
 }
 
@@ -280,7 +314,8 @@ IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t dvs, int 
 // not the byte pack's.  E8: every exponential fits a byte (I0 <= 255).
 template <bool FASTQ, bool NARROW, bool E8>
 __global__ void __launch_bounds__(kDiffThreads, 1)
-    attention_diff_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ DiffArgs a) {
+    attention_diff_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tmV,
+                          const __grid_constant__ DiffArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   const int N = a.N;
@@ -323,6 +358,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tm);
+    prefetch_tensormap(&tmV);
   }
   if (warp == 3) {
     __syncwarp();
@@ -366,12 +402,10 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
             tma_load_2d(q + (kQTile + 64 * i) * kHeadDim, &tm, D + col, row0 + 64 * i, &qk_full[s]);
         }
         if (!diff_wait(&v_empty[s], ph ^ 1, a.status, abort_flag)) break;
-        uint8_t* v = smem + L.v_off + s * L.v_bytes;  // two 64-wide halves
+        uint8_t* v = smem + L.v_off + s * L.v_bytes;
         mbar_arrive_expect_tx(&v_full[s], (uint32_t)L.v_bytes);
-        for (int m = 0; m < 2; ++m)
-          for (int i = 0; i < L.n64 / 64; ++i)
-            tma_load_2d(v + (m * L.n64 + 64 * i) * kHeadDim, &tm, 2 * D + h * kValDim + m * kHeadDim, row0 + 64 * i,
-                        &v_full[s]);
+        for (int i = 0; i < L.n64 / 64; ++i)
+          tma_load_2d(v + 64 * i * kValDim, &tmV, 2 * D + h * kValDim, row0 + 64 * i, &v_full[s]);
       }
     }
   } else if (warp <= 2) {
@@ -424,14 +458,12 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
           if (g == 1 && L.sep) ok = diff_wait(&p_full[1], ph, a.status, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t idesc = idesc_i8(kQTile, kHeadDim, g == 1, true, true);
+          const uint32_t idesc = idesc_i8(kQTile, kValDim, g == 1, true, true);
           const uint32_t pa = tmem + (uint32_t)(g * L.lcols);
           const uint32_t va = smem_u32(smem + L.v_off + s * L.v_bytes);
           for (int k = 0; k < L.n32 / 32; ++k)
-            for (int m = 0; m < 2; ++m)
-              umma_i8_ta(d_o + (uint32_t)(m * kHeadDim), pa + (uint32_t)(8 * k),
-                         smem_desc(va + (uint32_t)((m * L.n64 + 32 * k) * kHeadDim), 512, 512, kSwizzle64B), idesc,
-                         (uint32_t)(g | k));
+            umma_i8_ta(d_o, pa + (uint32_t)(8 * k),
+                       smem_desc(va + (uint32_t)(32 * k * kValDim), 1024, 1024, kSwizzle128B), idesc, (uint32_t)(g | k));
           umma_commit(&p_empty[g]);
         }
         if (!ok) break;
@@ -464,6 +496,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     // P = (Dv e) >> pshift in the top byte of (Dv << lsh) e >> rsh: |.| <= 2^(23 + k_out) <= 2^31
     const int pshift = a.M - (a.k_out - 1);
     const int lsh = max(24 - pshift, 0), rsh = max(pshift - 24, 0);
+    const uint32_t neg = g == 1 ? 0x7F7F7F7Fu : 0u;
     uint32_t n = 0;  // chunks seen
     bool ok = true;
     for (int j = 0; j < n_local; ++j) {
@@ -475,30 +508,42 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       if (g == 1) num = (uint32_t)min(max(__ldg(a.lam + h), 0), 1 << a.M);
 
       // ---- pass 1: maximum of the raw scores, 8-bit logits into TMEM
+      // (written once the chunk is read and the previous item's P has been consumed)
       int32_t mx = INT_MIN;
-      if (j > 0) {  // the previous item's P has been consumed
-        if (ok) ok = diff_wait(&p_empty[g], (uint32_t)((j - 1) & 1), a.status, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-      }
       for (int c = 0; c < L.nchunks; ++c, ++n) {
         if (ok) ok = diff_wait(&s_full[g], n & 1, a.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        const int k0 = c * L.chunk;
-        const int nu = min(L.chunk, L.n16 - k0) / 16;  // 16-key units, taken by the halves in turn
-        if (ok && rows)
-          stream_units<16>(t_s + (uint32_t)(16 * half), 32, (nu - half + 1) / 2, [&](uint32_t(&r)[16], int u) {
-            const int key = k0 + 16 * half + 32 * u;
-            uint32_t lw[4];
-            if (N - key >= 16)
-              logits16<FASTQ, NARROW, false>(r, 16, a, mx, lw);
-            else
-              logits16<FASTQ, NARROW, true>(r, N - key, a, mx, lw);
-            tmem_st4(t_l + (uint32_t)(key / 4), lw[0], lw[1], lw[2], lw[3]);
-          });
+        const int key0 = c * L.chunk + 16 * half;
+        const int nu = (min(L.chunk, L.n16 - c * L.chunk) / 16 - half + 1) / 2;  // 16-key units, taken by the halves in turn
+        uint32_t lw[kChunkUnits][4];
+        if (ok && rows) {
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u)
+            if (u < nu) {
+              uint32_t r[16];
+              tmem_ld16(t_s + (uint32_t)(16 * half + 32 * u), r);
+              tmem_ld_wait_regs(r);
+              const int lim = N - (key0 + 32 * u);
+              if (lim >= 16)
+                logits16<FASTQ, NARROW, false>(r, 16, a, mx, lw[u]);
+              else
+                logits16<FASTQ, NARROW, true>(r, lim, a, mx, lw[u]);
+            }
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[g]);
+        if (c == 0 && j > 0) {
+          if (ok) ok = diff_wait(&p_empty[g], (uint32_t)((j - 1) & 1), a.status, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+        }
+        if (ok && rows) {
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u)
+            if (u < nu) tmem_st4(t_l + (uint32_t)((key0 + 32 * u) / 4), lw[u][0], lw[u][1], lw[u][2], lw[u][3]);
+        }
       }
       if (rows) {
         tmem_st_wait();
@@ -532,14 +577,14 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
           if (rsh == 0)
             stream_units<8>(t_u, 8, u_n, [&](uint32_t(&r)[8], int u) {
               if (E8 || u != u_ragged)
-                prob32<E8, false, false>(r, 32, base, dvs, 0, g == 1);
+                prob32<E8, false, false>(r, 32, base, dvs, 0, neg);
               else
-                prob32<E8, false, true>(r, lim_ragged, base, dvs, 0, g == 1);
+                prob32<E8, false, true>(r, lim_ragged, base, dvs, 0, neg);
               tmem_st8(t_u + (uint32_t)(8 * u), r);
             });
           else
             stream_units<8>(t_u, 8, u_n, [&](uint32_t(&r)[8], int u) {
-              prob32<E8, true, true>(r, u != u_ragged ? 32 : lim_ragged, base, dvs, rsh, g == 1);
+              prob32<E8, true, true>(r, u != u_ragged ? 32 : lim_ragged, base, dvs, rsh, neg);
               tmem_st8(t_u + (uint32_t)(8 * u), r);
             });
         }
@@ -564,34 +609,10 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       if (ok && quarter * 32 < nrow) {
         const uint32_t t_o = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)L.o_col;
         int8_t* dst = a.ctx + (int64_t)(img * N + qt * a.qrows + row) * D + h * kValDim;
-#pragma unroll
-        for (int pr = 0; pr < 4; ++pr) {
-          uint32_t ra[16], rb[16];
-          tmem_ld16(t_o + (uint32_t)(32 * pr), ra);
-          tmem_ld16(t_o + (uint32_t)(32 * pr + 16), rb);
-          tmem_ld_wait_regs2(ra, rb);
-          if (row < nrow) {
-            uint32_t packed[8];
-#pragma unroll
-            for (int wd = 0; wd < 8; ++wd) {
-              int32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int32_t acc = (int32_t)(wd < 4 ? ra[wd * 4 + e] : rb[(wd - 4) * 4 + e]);
-                if (a.out_fast) {
-                  y[e] = __mulhi(a.out_bq, acc);  // floor(b_o acc / 2^c_o), exact
-                } else {
-                  const int32_t ac = min(max(acc, a.o_lo), a.o_hi);
-                  const int64_t v = (int64_t)a.out_b * ac;  // |v >> c| < 2^31 after the clamp
-                  y[e] = (int32_t)__funnelshift_r((uint32_t)v, (uint32_t)(v >> 32), (uint32_t)a.out_c);
-                }
-              }
-              packed[wd] = pack_sat4_diff(y[0], y[1], y[2], y[3]);
-            }
-            reinterpret_cast<int4*>(dst + 32 * pr)[0] = make_int4(packed[0], packed[1], packed[2], packed[3]);
-            reinterpret_cast<int4*>(dst + 32 * pr)[1] = make_int4(packed[4], packed[5], packed[6], packed[7]);
-          }
-        }
+        if (a.out_fast)
+          read_out<true>(t_o, row < nrow, dst, a);
+        else
+          read_out<false>(t_o, row < nrow, dst, a);
       }
       tc_fence_before();
       __syncwarp();
@@ -615,8 +636,10 @@ ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_
                                   const int32_t* lam, ivit_dyadic out, int8_t* ctx, cudaStream_t stream) {
   const int64_t T = (int64_t)B * N;
   const uint64_t width = (uint64_t)3 * kValDim * (uint64_t)H;
-  CUtensorMap tm;
-  const ivit_status st = encode_tmap_2d_u8(&tm, qkv, width, (uint64_t)T, width, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B);
+  CUtensorMap tm, tmV;  // boxes of 64 rows: 64 columns (Q, K) and 128 (V)
+  ivit_status st = encode_tmap_2d_u8(&tm, qkv, width, (uint64_t)T, width, kHeadDim, 64, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != IVIT_OK) return st;
+  st = encode_tmap_2d_u8(&tmV, qkv, width, (uint64_t)T, width, kValDim, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != IVIT_OK) return st;
   DiffArgs a{};
   a.B = B;
@@ -656,7 +679,7 @@ ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_
   if (items > 0x7fffffff) return IVIT_ERR_UNSUPPORTED;
   a.L = diff_layout(N);
   const int smem = a.L.total + 1024;
-  using Kernel = void (*)(CUtensorMap, DiffArgs);
+  using Kernel = void (*)(CUtensorMap, CUtensorMap, DiffArgs);
   static const Kernel kernels[8] = {
       attention_diff_kernel<false, false, false>, attention_diff_kernel<false, false, true>,
       attention_diff_kernel<false, true, false>,  attention_diff_kernel<false, true, true>,
@@ -671,7 +694,7 @@ ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_
     attr_done[dc.device] = true;
   }
   const unsigned grid = (unsigned)(items < dc.num_sms ? items : dc.num_sms);
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kDiffThreads), (size_t)smem, stream, tm, a);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kDiffThreads), (size_t)smem, stream, tm, tmV, a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
