@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
         const int s = j % L.depth;
         const uint32_t ph = (uint32_t)((j / L.depth) & 1);
         const int item = (int)blockIdx.x + j * (int)gridDim.x;
-        const int qt = item % qtiles, h = (item / qtiles) % a.H, img = item / (qtiles * a.H);
+        const int h = item % a.H, img = (item / a.H) % a.B, qt = item / (a.H * a.B);
         const int row0 = img * N;
         if (!diff_wait(&qk_empty[s], ph ^ 1, a.status, abort_flag)) break;
         uint8_t* st = smem + s * L.qk_bytes;
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     bool ok = true;
     for (int j = 0; j < n_local; ++j) {
       const int item = (int)blockIdx.x + j * (int)gridDim.x;
-      const int qt = item % qtiles, h = (item / qtiles) % a.H;
+      const int h = item % a.H, qt = item / (a.H * a.B);
       // warps whose rows all lie past the tile or the image's last token skip the passes
       const bool rows = quarter * 32 < min(a.qrows, N - qt * a.qrows);
       uint32_t num = 1u << a.M;  // IntDiv's numerator
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     bool ok = true;
     for (int j = 0; j < n_local; ++j) {
       const int item = (int)blockIdx.x + j * (int)gridDim.x;
-      const int qt = item % qtiles, h = (item / qtiles) % a.H, img = item / (qtiles * a.H);
+      const int h = item % a.H, img = (item / a.H) % a.B, qt = item / (a.H * a.B);
       if (ok) ok = diff_wait(o_full, (uint32_t)(j & 1), a.status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
