@@ -514,7 +514,9 @@ __device__ __forceinline__ void norm_row(int32_t s1, int32_t s2, int32_t cols, i
   muf = mu * f;
 }
 
-// the four normalised bytes of the word w of a row, requantised (not yet saturated)
+// the four normalised bytes of the word w of a row, requantised (not yet saturated);
+// FAST: n.fast holds
+template <bool FAST>
 __device__ __forceinline__ void norm_word(uint32_t w, int32_t f, int32_t muf, int sh, const int4& g4, const int4& b4,
                                           const NormArgs& n, int32_t lo, int32_t hi, int32_t (&r)[4]) {
   const int32_t gg[4] = {g4.x, g4.y, g4.z, g4.w};
@@ -523,7 +525,7 @@ __device__ __forceinline__ void norm_word(uint32_t w, int32_t f, int32_t muf, in
   for (int e = 0; e < 4; ++e) {
     const int32_t nv = (sext_byte(w, e) * f - muf) >> sh;
     const int32_t acc = nv * gg[e] + bb[e];
-    if (n.fast) {
+    if (FAST || n.fast) {
       r[e] = __mulhi(n.out_bq, acc);
     } else {
       const int64_t pr = (int64_t)n.out.b * min(max(acc, lo), hi);
@@ -551,7 +553,14 @@ __device__ __forceinline__ void stage_i32(int4* dst, const int32_t* t, int i, in
   dst[(i & 3) * nchunk + (i >> 2)] = __ldg(reinterpret_cast<const int4*>(t) + i);
 }
 
-template <int LPR, int CPL, bool POST, bool PRE>
+// The requants' forms and the gate are decided per launch, not per element (a
+// test inside the unrolled words doubled the instructions: 47.6 per element
+// and 21.8 us for 12608 x 768): kFormFast / kFormFastGate when both norms'
+// requants are one mul.hi and the residual sum's shift fits int32, without and
+// with a gate; kFormAny tests as it goes.
+enum ResNormForm : int { kFormAny = 0, kFormFast = 1, kFormFastGate = 2 };
+
+template <int LPR, int CPL, bool POST, bool PRE, int FORM>
 __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNormArgs a) {
   extern __shared__ int4 ln_smem[];
   const int cols = a.cols, nchunk = cols >> 4;
@@ -577,15 +586,17 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
   const int hl = threadIdx.x % LPR;
   constexpr int kRows = kLnThreads / LPR;
   int32_t plo = INT_MIN, phi = INT_MAX, nlo = INT_MIN, nhi = INT_MAX;
-  if (POST && !a.post.fast) out_bounds(a.post.out.b, a.post.out.c, plo, phi);
-  if (PRE && !a.pre.fast) out_bounds(a.pre.out.b, a.pre.out.c, nlo, nhi);
+  constexpr bool kFast = FORM != kFormAny;
+  if (POST && !kFast && !a.post.fast) out_bounds(a.post.out.b, a.post.out.c, plo, phi);
+  if (PRE && !kFast && !a.pre.fast) out_bounds(a.pre.out.b, a.pre.out.c, nlo, nhi);
   for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows; row0 += (int64_t)gridDim.x * kRows) {
     const int64_t row = row0 + threadIdx.x / LPR;
     const bool active = row < a.rows;
     const int64_t base = (active ? row : 0) * cols;
     const int4* xr = reinterpret_cast<const int4*>(a.skip + base);
     const int4* br = reinterpret_cast<const int4*>(a.branch + base);
-    const int4* gr = a.gate ? reinterpret_cast<const int4*>(a.gate + (active ? row / a.gate_rows : 0) * cols) : nullptr;
+    const bool gated = FORM == kFormFastGate || (FORM == kFormAny && a.gate);
+    const int4* gr = gated ? reinterpret_cast<const int4*>(a.gate + (active ? row / a.gate_rows : 0) * cols) : nullptr;
     int4 vx[CPL], vb[CPL];
     int32_t s1 = 0, s2 = 0;
 #pragma unroll
@@ -619,14 +630,14 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
         const uint32_t bw[4] = {(uint32_t)vb[k].x, (uint32_t)vb[k].y, (uint32_t)vb[k].z, (uint32_t)vb[k].w};
         const uint32_t xw[4] = {(uint32_t)vx[k].x, (uint32_t)vx[k].y, (uint32_t)vx[k].z, (uint32_t)vx[k].w};
         int4 gv = make_int4(0x01010101, 0x01010101, 0x01010101, 0x01010101);
-        if (gr) gv = __ldg(gr + ci);
+        if (gated) gv = __ldg(gr + ci);
         const uint32_t gw[4] = {(uint32_t)gv.x, (uint32_t)gv.y, (uint32_t)gv.z, (uint32_t)gv.w};
         uint32_t o[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           int32_t u[4];
           if (POST) {
-            norm_word(bw[q], f, muf, psh, s_pg[q * nchunk + ci], s_pb[q * nchunk + ci], a.post, plo, phi, u);
+            norm_word<kFast>(bw[q], f, muf, psh, s_pg[q * nchunk + ci], s_pb[q * nchunk + ci], a.post, plo, phi, u);
             const uint32_t pw = pack_sat4_ln(u[0], u[1], u[2], u[3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) u[e] = sext_byte(pw, e);
@@ -640,8 +651,9 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             // |sum| < 2^31 (2^7 + 2^14)
-            const int64_t t = (int64_t)a.b_skip * sext_byte(xw[q], e) + (int64_t)ss[e] * (u[e] * sext_byte(gw[q], e));
-            if (a.fast_res) {
+            const int32_t ug = FORM == kFormFast ? u[e] : u[e] * sext_byte(gw[q], e);
+            const int64_t t = (int64_t)a.b_skip * sext_byte(xw[q], e) + (int64_t)ss[e] * ug;
+            if (kFast || a.fast_res) {
               r[e] = (int32_t)__funnelshift_r((uint32_t)t, (uint32_t)(t >> 32), (uint32_t)a.c);
             } else {
               const int64_t v = t >> a.c;
@@ -671,7 +683,7 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             int32_t r[4];
-            norm_word(w[q], f, muf, nsh, s_ng[q * nchunk + ci], s_nb[q * nchunk + ci], a.pre, nlo, nhi, r);
+            norm_word<kFast>(w[q], f, muf, nsh, s_ng[q * nchunk + ci], s_nb[q * nchunk + ci], a.pre, nlo, nhi, r);
             o[q] = pack_sat4_ln(r[0], r[1], r[2], r[3]);
           }
           __stcs(reinterpret_cast<int4*>(a.z + base) + ci, make_int4((int)o[0], (int)o[1], (int)o[2], (int)o[3]));
@@ -693,24 +705,36 @@ NormArgs norm_args(const ivit_norm* n) {
                   fast ? 1 : 0};
 }
 
-template <int LPR, int CPL, bool POST, bool PRE>
+template <int LPR, int CPL, bool POST, bool PRE, int FORM>
 cudaError_t run_residual_norm(const DeviceCtx& dc, const ResNormArgs& a, cudaStream_t stream) {
   constexpr int kRows = kLnThreads / LPR;
   const size_t smem = (size_t)a.cols * 4 * (1 + (POST ? 2 : 0) + (PRE ? 2 : 0));  // at most 40 KB
-  auto kern = residual_norm_kernel<LPR, CPL, POST, PRE>;
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kLnThreads, smem) != cudaSuccess)
-    return cudaErrorUnknown;
+  auto kern = residual_norm_kernel<LPR, CPL, POST, PRE, FORM>;
   int64_t blocks = (a.rows + kRows - 1) / kRows;
-  const int64_t cap = (int64_t)dc.num_sms * (per_sm > 0 ? per_sm : 1);
-  if (blocks > cap) blocks = cap;
+  if (blocks > dc.num_sms) {  // as many blocks as fit at once, each walking rows
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kLnThreads, smem) != cudaSuccess)
+      return cudaErrorUnknown;
+    const int64_t cap = (int64_t)dc.num_sms * (per_sm > 0 ? per_sm : 1);
+    if (blocks > cap) blocks = cap;
+  }
   return launch_pdl(kern, dim3((unsigned)blocks), dim3(kLnThreads), smem, stream, a);
+}
+
+template <int LPR, int CPL, bool POST, bool PRE>
+cudaError_t run_residual_norm_form(const DeviceCtx& dc, const ResNormArgs& a, cudaStream_t stream) {
+  if (!a.fast_res || (POST && !a.post.fast) || (PRE && !a.pre.fast))
+    return run_residual_norm<LPR, CPL, POST, PRE, kFormAny>(dc, a, stream);
+  return a.gate ? run_residual_norm<LPR, CPL, POST, PRE, kFormFastGate>(dc, a, stream)
+                : run_residual_norm<LPR, CPL, POST, PRE, kFormFast>(dc, a, stream);
 }
 
 template <int LPR, int CPL>
 cudaError_t run_residual_norm_cpl(const DeviceCtx& dc, const ResNormArgs& a, bool post, bool pre, cudaStream_t stream) {
-  if (post) return pre ? run_residual_norm<LPR, CPL, true, true>(dc, a, stream) : run_residual_norm<LPR, CPL, true, false>(dc, a, stream);
-  return pre ? run_residual_norm<LPR, CPL, false, true>(dc, a, stream) : run_residual_norm<LPR, CPL, false, false>(dc, a, stream);
+  if (post) return pre ? run_residual_norm_form<LPR, CPL, true, true>(dc, a, stream)
+                       : run_residual_norm_form<LPR, CPL, true, false>(dc, a, stream);
+  return pre ? run_residual_norm_form<LPR, CPL, false, true>(dc, a, stream)
+             : run_residual_norm_form<LPR, CPL, false, false>(dc, a, stream);
 }
 
 }  // namespace
@@ -735,10 +759,10 @@ ivit_status launch_residual_norm(const DeviceCtx& dc, const int8_t* skip, const 
     e = run_residual_norm_cpl<kLnLanes, 3>(dc, a, po, pr, stream);
   else if (cpl <= 4)
     e = run_residual_norm_cpl<kLnLanes, 4>(dc, a, po, pr, stream);
-  else if (cpl <= 6)
-    e = run_residual_norm_cpl<kLnLanes, 6>(dc, a, po, pr, stream);
+  else if (cpl <= 6)  // past 1024 channels a whole warp per row, to stay within the registers
+    e = run_residual_norm_cpl<32, 3>(dc, a, po, pr, stream);
   else
-    e = run_residual_norm_cpl<kLnLanes, 8>(dc, a, po, pr, stream);
+    e = run_residual_norm_cpl<32, 4>(dc, a, po, pr, stream);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
