@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kPtfThreads)
 // registers between its two norms and is written once per output: half the
 // bytes of the separate operators.  kLnLanes lanes share a row as in
 // layernorm_staged_kernel; the per-channel tables are staged in shared memory
-// by each CTA, which then walks rows.
+// by each block, which then walks rows.
 // ---------------------------------------------------------------------------
 struct NormArgs {
   const int8_t* gamma;
@@ -560,8 +560,18 @@ __device__ __forceinline__ void stage_i32(int4* dst, const int32_t* t, int i, in
 // with a gate; kFormAny tests as it goes.
 enum ResNormForm : int { kFormAny = 0, kFormFast = 1, kFormFastGate = 2 };
 
+// One block per SM, so the per-channel tables are staged once per SM and every SM
+// walks the same number of rows (to within one per group of lanes).  Registers:
+// 80 per thread at three 16-byte chunks a lane, 128 at four.
+template <int CPL>
+constexpr int kResNormThreads = CPL <= 3 ? 768 : 512;
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int LPR, int CPL, bool POST, bool PRE, int FORM>
-__global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNormArgs a) {
+__global__ void __launch_bounds__(kResNormThreads<CPL>, 1) residual_norm_kernel(const ResNormArgs a) {
   extern __shared__ int4 ln_smem[];
   const int cols = a.cols, nchunk = cols >> 4;
   int4* const s_scale = ln_smem;  // [4][nchunk] each
@@ -569,6 +579,8 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
   int4* const s_pb = s_pg + (POST ? 4 * nchunk : 0);
   int4* const s_ng = s_pb + (POST ? 4 * nchunk : 0);
   int4* const s_nb = s_ng + (PRE ? 4 * nchunk : 0);
+  // a thread's own chunks of the next row it takes: [branch, skip, gate][chunk][thread]
+  int4* const s_next = s_nb + (PRE ? 4 * nchunk : 0) + threadIdx.x;
   for (int i = threadIdx.x; i < cols / 4; i += blockDim.x) {
     stage_i32(s_scale, a.scale, i, nchunk);
     if (POST) {
@@ -584,27 +596,48 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
   pdl_wait();  // skip, branch and gate come from earlier kernels
   pdl_launch_dependents();
   const int hl = threadIdx.x % LPR;
-  constexpr int kRows = kLnThreads / LPR;
-  int32_t plo = INT_MIN, phi = INT_MAX, nlo = INT_MIN, nhi = INT_MAX;
+  const int groups = blockDim.x / LPR;  // rows in hand at once
   constexpr bool kFast = FORM != kFormAny;
+  const bool gated = FORM == kFormFastGate || (FORM == kFormAny && a.gate);
+  int32_t plo = INT_MIN, phi = INT_MAX, nlo = INT_MIN, nhi = INT_MAX;
   if (POST && !kFast && !a.post.fast) out_bounds(a.post.out.b, a.post.out.c, plo, phi);
   if (PRE && !kFast && !a.pre.fast) out_bounds(a.pre.out.b, a.pre.out.c, nlo, nhi);
-  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows; row0 += (int64_t)gridDim.x * kRows) {
-    const int64_t row = row0 + threadIdx.x / LPR;
+  // The next row's chunks are on their way to shared memory while a row is
+  // worked on; each thread fetches and reads its own, so nothing is waited for
+  // but its own copies.
+  auto fetch = [&](int64_t row) {
+    if (row < a.rows) {
+      const int8_t* g = gated ? a.gate + row / a.gate_rows * cols : nullptr;
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) {
+        const int ci = hl + LPR * k;
+        if (ci < nchunk) {
+          copy16_async(smem_u32(s_next + k * blockDim.x), a.branch + row * cols + 16 * ci);
+          copy16_async(smem_u32(s_next + (CPL + k) * blockDim.x), a.skip + row * cols + 16 * ci);
+          if (gated) copy16_async(smem_u32(s_next + (2 * CPL + k) * blockDim.x), g + 16 * ci);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // row = (group of lanes) * blocks + block: the rows of a block lie apart, but
+  // every block has as many as any other
+  const int64_t step = (int64_t)groups * gridDim.x;
+  int64_t row = (int64_t)(threadIdx.x / LPR) * gridDim.x + blockIdx.x;
+  fetch(row);
+  for (int64_t row0 = blockIdx.x; row0 < a.rows; row0 += step, row += step) {  // the same trips for a warp's lanes
     const bool active = row < a.rows;
     const int64_t base = (active ? row : 0) * cols;
-    const int4* xr = reinterpret_cast<const int4*>(a.skip + base);
-    const int4* br = reinterpret_cast<const int4*>(a.branch + base);
-    const bool gated = FORM == kFormFastGate || (FORM == kFormAny && a.gate);
-    const int4* gr = gated ? reinterpret_cast<const int4*>(a.gate + (active ? row / a.gate_rows : 0) * cols) : nullptr;
-    int4 vx[CPL], vb[CPL];
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    int4 vx[CPL], vb[CPL], vg[CPL];
     int32_t s1 = 0, s2 = 0;
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
       const int ci = hl + LPR * k;
       if (active && ci < nchunk) {
-        vb[k] = __ldcs(br + ci);
-        vx[k] = __ldcs(xr + ci);
+        vb[k] = s_next[k * blockDim.x];
+        vx[k] = s_next[(CPL + k) * blockDim.x];
+        vg[k] = gated ? s_next[(2 * CPL + k) * blockDim.x] : make_int4(0x01010101, 0x01010101, 0x01010101, 0x01010101);
         if (POST) {
           const int w[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
 #pragma unroll
@@ -615,6 +648,7 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
         }
       }
     }
+    fetch(row + step);
     int32_t f = 0, muf = 0;
     if (POST) {
       row_sum2<LPR>(s1, s2);
@@ -629,9 +663,7 @@ __global__ void __launch_bounds__(kLnThreads) residual_norm_kernel(const ResNorm
       if (active && ci < nchunk) {
         const uint32_t bw[4] = {(uint32_t)vb[k].x, (uint32_t)vb[k].y, (uint32_t)vb[k].z, (uint32_t)vb[k].w};
         const uint32_t xw[4] = {(uint32_t)vx[k].x, (uint32_t)vx[k].y, (uint32_t)vx[k].z, (uint32_t)vx[k].w};
-        int4 gv = make_int4(0x01010101, 0x01010101, 0x01010101, 0x01010101);
-        if (gated) gv = __ldg(gr + ci);
-        const uint32_t gw[4] = {(uint32_t)gv.x, (uint32_t)gv.y, (uint32_t)gv.z, (uint32_t)gv.w};
+        const uint32_t gw[4] = {(uint32_t)vg[k].x, (uint32_t)vg[k].y, (uint32_t)vg[k].z, (uint32_t)vg[k].w};
         uint32_t o[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -707,18 +739,20 @@ NormArgs norm_args(const ivit_norm* n) {
 
 template <int LPR, int CPL, bool POST, bool PRE, int FORM>
 cudaError_t run_residual_norm(const DeviceCtx& dc, const ResNormArgs& a, cudaStream_t stream) {
-  constexpr int kRows = kLnThreads / LPR;
-  const size_t smem = (size_t)a.cols * 4 * (1 + (POST ? 2 : 0) + (PRE ? 2 : 0));  // at most 40 KB
   auto kern = residual_norm_kernel<LPR, CPL, POST, PRE, FORM>;
-  int64_t blocks = (a.rows + kRows - 1) / kRows;
-  if (blocks > dc.num_sms) {  // as many blocks as fit at once, each walking rows
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kLnThreads, smem) != cudaSuccess)
-      return cudaErrorUnknown;
-    const int64_t cap = (int64_t)dc.num_sms * (per_sm > 0 ? per_sm : 1);
-    if (blocks > cap) blocks = cap;
+  // few rows: smaller blocks, so that more SMs share them
+  const int threads = a.rows * LPR <= (int64_t)256 * dc.num_sms ? 256 : kResNormThreads<CPL>;
+  const size_t smem = (size_t)a.cols * 4 * (1 + (POST ? 2 : 0) + (PRE ? 2 : 0)) +
+                      (size_t)threads * 16 * CPL * (FORM == kFormFast ? 2 : 3);  // at most 136 KB
+  static bool attr_done[64];  // per device; benign race: the attribute value is the same
+  if (!attr_done[dc.device]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) return e;
+    attr_done[dc.device] = true;
   }
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(kLnThreads), smem, stream, a);
+  const int groups = threads / LPR;
+  const int64_t blocks = (a.rows + groups - 1) / groups;
+  return launch_pdl(kern, dim3((unsigned)(blocks < dc.num_sms ? blocks : dc.num_sms)), dim3(threads), smem, stream, a);
 }
 
 template <int LPR, int CPL, bool POST, bool PRE>
@@ -757,9 +791,9 @@ ivit_status launch_residual_norm(const DeviceCtx& dc, const int8_t* skip, const 
     e = run_residual_norm_cpl<kLnLanes, 2>(dc, a, po, pr, stream);
   else if (cpl <= 3)
     e = run_residual_norm_cpl<kLnLanes, 3>(dc, a, po, pr, stream);
-  else if (cpl <= 4)
-    e = run_residual_norm_cpl<kLnLanes, 4>(dc, a, po, pr, stream);
-  else if (cpl <= 6)  // past 1024 channels a whole warp per row, to stay within the registers
+  else if (cpl <= 4)  // past 768 channels a whole warp per row, to stay within the registers
+    e = run_residual_norm_cpl<32, 2>(dc, a, po, pr, stream);
+  else if (cpl <= 6)
     e = run_residual_norm_cpl<32, 3>(dc, a, po, pr, stream);
   else
     e = run_residual_norm_cpl<32, 4>(dc, a, po, pr, stream);
