@@ -52,17 +52,20 @@
 // and a parity wait cannot tell phase p from phase p + 2).  At BN = 256 the
 // ring is three deep and a single thread keeps the tensor core busy.
 //
-// Low-rank adapters of many requests (LORA, ivit_linear_lora): after a tile's
-// k-slices come its adapter stages.  t = requant(X A_a^T) [M x R] has been
-// written by the kernel before; request q's rows of it and its adapter's
-// B_a [N x R] are one more stretch of reduction, sum_r t_ir B_a[j, r], that
-// accumulates onto the same TMEM tile, so every epilogue applies unchanged.
-// The rows of other requests must not see B_a: t is loaded through a tensor
-// map [request, row of request, R], whose bounds zero-fill every token of the
-// tile outside request q, and a request without an adapter loads B_a from
-// outside the map, zero as well.  One ring stage holds up to four such
-// 32-byte chunks (32B swizzle, 128 x 32 B of B_a and BN x 32 B of t each), so
-// a tile of two or three requests of rank up to 32 pays for one stage.
+// Low-rank adapters of many requests (ivit_linear_lora): the accumulator also
+// takes sum_r t_ir B_a[j, r], a the adapter of token i's request and t =
+// requant(X A_a^T) [M x R], which the kernel before has written; every epilogue
+// then applies unchanged.  Two ways, chosen by the launcher (see lora_kind):
+//   kLoraMma   requests of many tokens: after a tile's k-slices come further
+//              ones whose reduction axis is [request of the tile][rank].  B_a
+//              of each request lies there as it is, t block-diagonally (zero
+//              in other requests' columns).  That layout is in no tensor, and
+//              boxes of R bytes cost TMA as much per row as 128-byte ones (as
+//              tensor maps per request, zero-filled past its rows, the slices
+//              took 8 us of a 27 us ViT-B QKV), so warp 15 fills these stages
+//              with 16-byte cp.async, whose source size of zero writes zeros;
+//   kLoraEpi   requests of few tokens, where the axis would be mostly zeros:
+//              the epilogue warps add t . B_a to the accumulators with dp4a.
 #include <climits>
 
 #include "ivit_common.cuh"
@@ -93,47 +96,134 @@ struct GemmArgs {
   int32_t withhold;  // diagnostic: CTA 0's producer stops before this k-slice of its sequence (-1: never)
 };
 
-// The adapter operands of a LORA launch (see above); empty without.
-constexpr int kLoraChunk = 32;           // bytes = rank entries per chunk, one MMA k-step
-constexpr int kLoraPerStage = kBK / kLoraChunk;
-template <bool LORA>
-struct LoraOperands {};
-template <>
-struct LoraOperands<true> {
-  CUtensorMap T;        // t: (R, rows, requests), box 32 x BN x 1
-  CUtensorMap B;        // B: (R, N, adapters), box 32 x 128 x 1
-  const int32_t* idx;   // adapter of each request
-  uint32_t rows;        // tokens per request
-  int32_t n;            // adapters
-  int32_t chunks;       // ceil(R / 32)
+// The adapters of a launch (see above); empty without.
+enum LoraKind : int { kLoraNone = 0, kLoraMma = 1, kLoraEpi = 2 };
+template <int LORA>
+struct LoraArgs {
+  const int8_t* T;     // [M x R]
+  const int8_t* B;     // [n x N x R]
+  const int32_t* idx;  // adapter of each request
+  uint32_t rows;       // tokens per request
+  int32_t n, R;
 };
+template <>
+struct LoraArgs<kLoraNone> {};
 
-// First request and number of chunks (requests x rank chunks) of the token
-// tile [first, first + BN).
+template <int LORA>
+constexpr int gemm_threads() {
+  return kGemmThreads + (LORA == kLoraMma ? 32 : 0);
+}
+
+// First request of the token tile [tb BN, ...) and the 16-byte pieces of its
+// adapter axis.
 template <int BN>
-IVIT_DEV void lora_span(const LoraOperands<true>& lo, int64_t M, int tb, uint32_t& q0, int& total) {
+IVIT_DEV void lora_span(const LoraArgs<kLoraMma>& lo, int64_t M, int tb, uint32_t& q0, int& pieces) {
   const uint32_t first = (uint32_t)tb * (uint32_t)BN;  // M < 2^31
   const uint32_t last = min(first + (uint32_t)BN, (uint32_t)M) - 1u;
   q0 = first / lo.rows;
-  total = (int)(last / lo.rows - q0 + 1u) * lo.chunks;
+  pieces = (int)(last / lo.rows - q0 + 1u) * (lo.R / 16);
+}
+constexpr int kPiecesPerStage = kBK / 16;
+
+// k-slices of a tile, the adapters' included, and the MMA steps of 32 bytes in slice kb
+template <int BN, int LORA>
+IVIT_DEV int tile_slices(const LoraArgs<LORA>& lo, int64_t M, int tb, int num_kb, int& pieces) {
+  pieces = 0;
+  if constexpr (LORA == kLoraMma) {
+    uint32_t q0;
+    lora_span<BN>(lo, M, tb, q0, pieces);
+    return num_kb + (pieces + kPiecesPerStage - 1) / kPiecesPerStage;
+  }
+  return num_kb;
 }
 
-// Loads adapter stage k of the tile: chunks [4 k, 4 k + 4) of its span.
-template <int BN>
-IVIT_DEV void lora_load_stage(const LoraOperands<true>& lo, int k, int cb, int tb, uint32_t q0, int total,
-                              uint8_t* sa, int a_bytes, uint64_t* full) {
-  const int u0 = k * kLoraPerStage;
-  const int nu = min(kLoraPerStage, total - u0);
-  mbar_arrive_expect_tx(full, (uint32_t)(nu * (kBM + BN) * kLoraChunk));
-  for (int i = 0; i < nu; ++i) {
-    const int u = u0 + i;
-    const int r = u / lo.chunks, cc = u - r * lo.chunks;
-    const uint32_t q = q0 + (uint32_t)r;
-    int32_t a = __ldg(lo.idx + q);
-    if (a < 0 || a >= lo.n) a = -1;  // outside the map: B loads as zeros
-    tma_load_3d(sa + i * (kBM * kLoraChunk), &lo.B, cc * kLoraChunk, cb * kBM, a, full);
-    tma_load_3d(sa + a_bytes + i * (BN * kLoraChunk), &lo.T, cc * kLoraChunk,
-                (int32_t)((int64_t)tb * BN - (int64_t)q * lo.rows), (int32_t)q, full);
+IVIT_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+
+// Warp 15: the adapter stages of every tile of this CTA.  Piece u of the axis is
+// rank entries [16 (u % P), + 16) of request q0 + u / P, P = R / 16; both
+// operands' rows are 128 bytes, 128B-swizzled, as TMA would leave them.  A last
+// odd piece gets a partner of zeros in t (an MMA step takes 32 bytes; whatever
+// B's half of it holds is then multiplied by zero), and so does a request
+// without an adapter.
+//
+// The TMA warp, which alone goes through the ring slice by slice, waits until a
+// stage is empty and hands it over through grant[stage]: a wait on `empty` from
+// here could be whole phases ahead or behind, which a parity cannot tell.  A
+// stage is granted again only after its last filling has been consumed, so each
+// grant barrier is at most one phase ahead of the parity kept here.
+template <int BN, int STAGES, int kABytes, int kStageBytes>
+IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int num_kb, int ch_tiles, int num_tiles,
+                        uint8_t* smem, uint64_t* full, uint64_t* grant, int* status) {
+  const int lane = threadIdx.x & 31;
+  const int P = lo.R / 16;
+  uint32_t pos = 0;   // slices of this CTA's sequence so far
+  uint32_t used = 0;  // bit s: parity of stage s's grants so far
+  for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+    const int cb = t % ch_tiles, tb = t / ch_tiles;
+    const int64_t tok0 = (int64_t)tb * BN;
+    uint32_t q0;
+    int pieces;
+    lora_span<BN>(lo, M, tb, q0, pieces);
+    pos += (uint32_t)num_kb;
+    for (int u0 = 0; u0 < pieces; u0 += kPiecesPerStage, ++pos) {
+      const int stage = (int)(pos % STAGES);
+      if (!__all_sync(0xffffffffu, mbar_wait(&grant[stage], (used >> stage) & 1u, status))) return;
+      used ^= 1u << stage;
+      const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+      const int np = min(kPiecesPerStage, pieces - u0);
+      for (int i = 0; i < ((np + 1) & ~1); ++i) {
+        const int r = (u0 + i) / P, part = (u0 + i) - r * P;
+        const int64_t q = (int64_t)q0 + r;
+        const int32_t a = i < np ? __ldg(lo.idx + q) : -1;
+        const bool has = a >= 0 && a < lo.n;
+        if (has) {
+          const int8_t* b = lo.B + ((int64_t)a * N + cb * kBM + lane) * lo.R + 16 * part;
+#pragma unroll
+          for (int k = 0; k < kBM / 32; ++k) {
+            const int ch = lane + 32 * k;
+            if (cb * kBM + ch < N)
+              cp_async16_zfill(sa + (uint32_t)(ch * kBK + ((i ^ (ch & 7)) << 4)), b + (int64_t)(32 * k) * lo.R, true);
+          }
+        }
+        // the request's rows within the tile
+        const int lo_row = (int)(q * lo.rows - tok0), hi_row = lo_row + (int)lo.rows;
+#pragma unroll
+        for (int k = 0; k < (BN + 31) / 32; ++k) {
+          const int row = lane + 32 * k;
+          const bool take = has && row >= lo_row && row < hi_row;
+          if (BN % 32 == 0 || row < BN)
+            cp_async16_zfill(sb + (uint32_t)(row * kBK + ((i ^ (row & 7)) << 4)),
+                             lo.T + (take ? (tok0 + row) * lo.R + 16 * part : 0), take);
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[stage]);
+    }
+  }
+}
+
+// The epilogue's own adapters: r[i] += t . B_a of token tok0 + i and channel ch.
+IVIT_DEV void lora_add(uint32_t (&r)[16], const LoraArgs<kLoraEpi>& lo, int64_t M, int N, int64_t tok0, int ch) {
+  const int lane = threadIdx.x & 31;
+  const int64_t tok = tok0 + (lane & 15);
+  int32_t mine = tok < M ? __ldg(lo.idx + (uint32_t)tok / lo.rows) : -1;
+  if (mine >= lo.n) mine = -1;
+  const int8_t* b0 = lo.B + (int64_t)min(ch, N - 1) * lo.R;
+  const int64_t bstep = (int64_t)N * lo.R;
+  for (int p = 0; p < lo.R; p += 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int32_t a = __shfl_sync(0xffffffffu, mine, i);
+      // without an adapter (or past the last token): any row, not added
+      const int4 tv = *reinterpret_cast<const int4*>(lo.T + min(tok0 + i, M - 1) * lo.R + p);
+      const int4 bv = __ldg(reinterpret_cast<const int4*>(b0 + max(a, 0) * bstep + p));
+      const int32_t s = __dp4a(tv.x, bv.x, __dp4a(tv.y, bv.y, __dp4a(tv.z, bv.z, __dp4a(tv.w, bv.w, 0))));
+      r[i] += a >= 0 ? (uint32_t)s : 0u;
+    }
   }
 }
 
@@ -352,11 +442,22 @@ IVIT_DEV void epi_chunk(const uint32_t (&r)[16], const ChanConst& kc, const Gemm
 
 // The chunks [c_begin, c_begin + n) of one tile into the part's slots, two
 // chunks' TMEM loads per wait.
-template <int EPI, bool NARROW, int REQ>
+template <int EPI, bool NARROW, int REQ, int LORA>
 IVIT_DEV void epi_tile(uint32_t tbase, int c_begin, int n, const ChanConst& kc, const GemmArgs& args,
                        const int8_t* gelu_tab, uint8_t* slots, uint32_t ofs_even, uint32_t ofs_odd, uint32_t sel2,
-                       uint32_t sel1) {
+                       uint32_t sel1, [[maybe_unused]] const LoraArgs<LORA>& lora, [[maybe_unused]] int64_t tok_base,
+                       [[maybe_unused]] int ch) {
   const uint32_t t0 = tbase + (uint32_t)(16 * c_begin);
+  if constexpr (LORA == kLoraEpi) {
+    for (int i = 0; i < n; ++i) {
+      uint32_t r[16];
+      tmem_ld16(t0 + (uint32_t)(16 * i), r);
+      tmem_ld_wait_regs(r);
+      lora_add(r, lora, args.M, args.N, tok_base + 16 * (c_begin + i), ch);
+      epi_chunk<EPI, NARROW, REQ>(r, kc, args, gelu_tab, slots + i * kSlotBytes, ofs_even, ofs_odd, sel2, sel1);
+    }
+    return;
+  }
   int i = 0;
   for (; i + 1 < n; i += 2) {
     uint32_t ra[16], rb[16];
@@ -395,11 +496,11 @@ IVIT_DEV void bias_fill(uint32_t tbase, int c_begin, int c_end, int32_t bias) {
   for (int cc = c_begin; cc < c_end; ++cc) tmem_st16_fill(tbase + (uint32_t)(16 * cc), (uint32_t)bias);
 }
 
-template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+template <int BN, int STAGES, int EPI, bool NARROW, int LORA>
+__global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     gemm_i8_requant_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                            const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS,
-                           const __grid_constant__ LoraOperands<LORA> lora, const GemmArgs args) {
+                           const __grid_constant__ LoraArgs<LORA> lora, const GemmArgs args) {
   using L = GemmLayout<BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -411,6 +512,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* skip_full = drain + 1;  // [kEpiParts]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   int8_t* gelu_tab = reinterpret_cast<int8_t*>(smem + L::kGeluOff);
+  [[maybe_unused]] uint64_t* grant = reinterpret_cast<uint64_t*>(smem + L::kBytes);  // [STAGES], kLoraMma only
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -425,6 +527,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      if (LORA == kLoraMma) mbar_init(&grant[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], L::kIssuers);  // one commit per issuing thread
@@ -437,10 +540,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmY);
     if (EPI == kEpiResidual) prefetch_tensormap(&tmS);
-    if constexpr (LORA) {
-      prefetch_tensormap(&lora.T);
-      prefetch_tensormap(&lora.B);
-    }
   }
   if (EPI == kEpiGelu) {
     for (int i = threadIdx.x; i < 256; i += blockDim.x)
@@ -456,7 +555,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tslot;
-  pdl_wait();  // X and the skip tensor come from earlier kernels
+  pdl_wait();  // X, the skip tensor and t come from earlier kernels
   pdl_launch_dependents();
 
   if (warp == 0) {
@@ -468,14 +567,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int issued = 0;  // k-slices loaded so far by this CTA
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const int cb = t % ch_tiles, tb = t / ch_tiles;
-        int tile_kb = num_kb;
-        [[maybe_unused]] uint32_t q0 = 0;
-        [[maybe_unused]] int lora_total = 0;
-        if constexpr (LORA) {
-          lora_span<BN>(lora, M, tb, q0, lora_total);
-          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
-        }
-        for (int kb = 0; kb < tile_kb; ++kb, ++issued) {
+        for (int kb = 0; kb < num_kb; ++kb, ++issued) {
           if (!mbar_wait(&empty[stage], phase ^ 1, args.status)) {
             ok = false;
             break;
@@ -487,17 +579,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           }
           uint8_t* sa = smem + stage * L::kStageBytes;
-          if (LORA && kb >= num_kb) {
-            if constexpr (LORA)
-              lora_load_stage<BN>(lora, kb - num_kb, cb, tb, q0, lora_total, sa, L::kABytes, &full[stage]);
-          } else {
-            mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
-            tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
-            tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
-          }
+          mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
+          tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
+          tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
+          }
+        }
+        if constexpr (LORA == kLoraMma) {  // the adapter stages go to warp 15
+          int pieces;
+          for (int kb = tile_slices<BN, LORA>(lora, M, tb, num_kb, pieces); kb > num_kb && ok; --kb) {
+            ok = mbar_wait(&empty[stage], phase ^ 1, args.status);
+            if (ok) mbar_arrive(&grant[stage]);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
       }
@@ -512,9 +610,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // loop stays a handful of instructions per MMA
       const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint32_t d_lo0 = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
-      // adapter chunks: rows of 32 bytes, 8-row groups of 256 bytes; the low
-      // half (start address, leading offset) is that of the k-slices
-      [[maybe_unused]] const uint32_t d_hi32 = (uint32_t)(smem_desc(0, 16, 256, kSwizzle32B) >> 32);
       // this thread takes every kStep-th k-slice of the CTA's sequence,
       // starting with slice warp - 1; the ring position advances kStep stages
       // per slice
@@ -529,13 +624,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!mbar_wait(&tempty[acc], acc_phase, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * L::kAccCols);
-        int tile_kb = num_kb;
-        [[maybe_unused]] int lora_total = 0;
-        if constexpr (LORA) {
-          uint32_t q0;
-          lora_span<BN>(lora, M, t / ch_tiles, q0, lora_total);
-          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
-        }
+        [[maybe_unused]] int pieces;
+        const int tile_kb = LORA == kLoraMma ? tile_slices<BN, LORA>(lora, M, t / ch_tiles, num_kb, pieces) : num_kb;
         int kb = kb0;
         for (; kb < tile_kb; kb += kStep) {
           if (!mbar_wait(&full[stage], phase, args.status)) {
@@ -545,11 +635,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tc_fence_after();
           const uint32_t a_lo = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
           const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
-          if (LORA && kb >= num_kb) {
-            const int nu = min(kLoraPerStage, lora_total - (kb - num_kb) * kLoraPerStage);
-            for (int i = 0; i < nu; ++i)
-              umma_i8_acc(d_tmem, a_lo + i * (kBM * kLoraChunk >> 4), d_hi32, b_lo + i * (BN * kLoraChunk >> 4),
-                          d_hi32, idesc);
+          if (LORA == kLoraMma && kb >= num_kb) {
+            const int steps = (min(kPiecesPerStage, pieces - (kb - num_kb) * kPiecesPerStage) + 1) / 2;
+            for (int k = 0; k < steps; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
           } else {
 #pragma unroll
             for (int k = 0; k < kBK / 32; ++k)  // accumulate onto the preloaded bias
@@ -573,6 +661,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       umma_commit(drain);
       mbar_wait(drain, 0, args.status);
     }
+  } else if (LORA == kLoraMma && warp == 3 + kEpiWarps) {
+    // ------------------------------------------------------------ adapter stages
+    if constexpr (LORA == kLoraMma)
+      lora_fill<BN, STAGES, L::kABytes, L::kStageBytes>(lora, M, N, num_kb, ch_tiles, num_tiles, smem, full, grant,
+                                                        args.status);
   } else {
     // ------------------------------------------------------------ epilogue
     constexpr int kChunks = L::kChunks;
@@ -687,7 +780,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const uint32_t tbase = tlane + (uint32_t)(acc * L::kAccCols);
 #define IVIT_EPI_TILE(R) \
-  epi_tile<EPI, NARROW, R>(tbase, c_begin, n, kc, args, gelu_tab, slots, ofs_even, ofs_odd, sel2, sel1)
+  epi_tile<EPI, NARROW, R, LORA>(tbase, c_begin, n, kc, args, gelu_tab, slots, ofs_even, ofs_odd, sel2, sel1, lora, \
+                                 tok_base, cb * kBM + quarter * 32 + lane)
       if (!args.round) {
         if (req == kReqFast)
           IVIT_EPI_TILE(kReqFast);
@@ -777,11 +871,11 @@ struct OwnLayout {
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
 };
 
-template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+template <int BN, int STAGES, int EPI, bool NARROW, int LORA>
+__global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     gemm_own_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS,
-                    const __grid_constant__ LoraOperands<LORA> lora, const GemmArgs args) {
+                    const __grid_constant__ LoraArgs<LORA> lora, const GemmArgs args) {
   using L = OwnLayout<BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -793,6 +887,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* skip_full = drain + 1;       // [kEpiParts]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   int8_t* gelu_tab = reinterpret_cast<int8_t*>(smem + L::kGeluOff);
+  [[maybe_unused]] uint64_t* grant = reinterpret_cast<uint64_t*>(smem + L::kBytes);  // [STAGES], kLoraMma only
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -807,6 +902,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      if (LORA == kLoraMma) mbar_init(&grant[s], 1);
     }
     for (int a = 0; a < kOwnAcc; ++a) {
       mbar_init(&tfull[a], L::kIssuers);  // one commit per issuing thread
@@ -819,10 +915,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmY);
     if (EPI == kEpiResidual) prefetch_tensormap(&tmS);
-    if constexpr (LORA) {
-      prefetch_tensormap(&lora.T);
-      prefetch_tensormap(&lora.B);
-    }
   }
   if (EPI == kEpiGelu) {
     for (int i = threadIdx.x; i < 256; i += blockDim.x)
@@ -838,7 +930,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tslot;
-  pdl_wait();  // X and the skip tensor come from earlier kernels
+  pdl_wait();  // X, the skip tensor and t come from earlier kernels
   pdl_launch_dependents();
 
   if (warp == 0) {
@@ -850,14 +942,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int issued = 0;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const int cb = t % ch_tiles, tb = t / ch_tiles;
-        int tile_kb = num_kb;
-        [[maybe_unused]] uint32_t q0 = 0;
-        [[maybe_unused]] int lora_total = 0;
-        if constexpr (LORA) {
-          lora_span<BN>(lora, M, tb, q0, lora_total);
-          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
-        }
-        for (int kb = 0; kb < tile_kb; ++kb, ++issued) {
+        for (int kb = 0; kb < num_kb; ++kb, ++issued) {
           if (!mbar_wait(&empty[stage], phase ^ 1, args.status)) {
             ok = false;
             break;
@@ -867,17 +952,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           }
           uint8_t* sa = smem + stage * L::kStageBytes;
-          if (LORA && kb >= num_kb) {
-            if constexpr (LORA)
-              lora_load_stage<BN>(lora, kb - num_kb, cb, tb, q0, lora_total, sa, L::kABytes, &full[stage]);
-          } else {
-            mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
-            tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
-            tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
-          }
+          mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
+          tma_load_2d(sa, &tmW, kb * kBK, cb * kBM, &full[stage]);
+          tma_load_2d(sa + L::kABytes, &tmX, kb * kBK, tb * BN, &full[stage]);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
+          }
+        }
+        if constexpr (LORA == kLoraMma) {  // the adapter stages go to warp 15
+          int pieces;
+          for (int kb = tile_slices<BN, LORA>(lora, M, tb, num_kb, pieces); kb > num_kb && ok; --kb) {
+            ok = mbar_wait(&empty[stage], phase ^ 1, args.status);
+            if (ok) mbar_arrive(&grant[stage]);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
       }
@@ -889,9 +980,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t idesc = idesc_i8(kBM, BN, true, true, false);
       const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint32_t d_lo0 = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
-      // adapter chunks: rows of 32 bytes, 8-row groups of 256 bytes; the low
-      // half (start address, leading offset) is that of the k-slices
-      [[maybe_unused]] const uint32_t d_hi32 = (uint32_t)(smem_desc(0, 16, 256, kSwizzle32B) >> 32);
       int stage = warp - 1;
       uint32_t phase = 0;
       int kb0 = warp - 1;
@@ -902,13 +990,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (!mbar_wait(&tempty[acc], acc_phase, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * L::kAccCols);
-        int tile_kb = num_kb;
-        [[maybe_unused]] int lora_total = 0;
-        if constexpr (LORA) {
-          uint32_t q0;
-          lora_span<BN>(lora, M, t / ch_tiles, q0, lora_total);
-          tile_kb += (lora_total + kLoraPerStage - 1) / kLoraPerStage;
-        }
+        [[maybe_unused]] int pieces;
+        const int tile_kb = LORA == kLoraMma ? tile_slices<BN, LORA>(lora, M, t / ch_tiles, num_kb, pieces) : num_kb;
         int kb = kb0;
         for (; kb < tile_kb; kb += kStep) {
           if (!mbar_wait(&full[stage], phase, args.status)) {
@@ -918,11 +1001,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tc_fence_after();
           const uint32_t a_lo = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
           const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
-          if (LORA && kb >= num_kb) {
-            const int nu = min(kLoraPerStage, lora_total - (kb - num_kb) * kLoraPerStage);
-            for (int i = 0; i < nu; ++i)
-              umma_i8_acc(d_tmem, a_lo + i * (kBM * kLoraChunk >> 4), d_hi32, b_lo + i * (BN * kLoraChunk >> 4),
-                          d_hi32, idesc);
+          if (LORA == kLoraMma && kb >= num_kb) {
+            const int steps = (min(kPiecesPerStage, pieces - (kb - num_kb) * kPiecesPerStage) + 1) / 2;
+            for (int k = 0; k < steps; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
           } else {
 #pragma unroll
             for (int k = 0; k < kBK / 32; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
@@ -945,6 +1026,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       umma_commit(drain);
       mbar_wait(drain, 0, args.status);
     }
+  } else if (LORA == kLoraMma && warp == 3 + kEpiWarps) {
+    // ------------------------------------------------------------ adapter stages
+    if constexpr (LORA == kLoraMma)
+      lora_fill<BN, STAGES, L::kABytes, L::kStageBytes>(lora, M, N, num_kb, ch_tiles, num_tiles, smem, full, grant,
+                                                        args.status);
   } else {
     // ------------------------------------------------------------ epilogue
     constexpr int kChunks = L::kChunks;
@@ -1021,7 +1107,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       tc_fence_after();
 #define IVIT_OWN_TILE(R) \
-  epi_tile<EPI, NARROW, R>(tbase, 0, n, kc, args, gelu_tab, slots, ofs_even, ofs_odd, sel2, sel1)
+  epi_tile<EPI, NARROW, R, LORA>(tbase, 0, n, kc, args, gelu_tab, slots, ofs_even, ofs_odd, sel2, sel1, lora, \
+                                 tok_base, cb * kBM + quarter * 32 + lane)
       if (!args.round) {
         if (req == kReqFast)
           IVIT_OWN_TILE(kReqFast);
@@ -1068,26 +1155,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// The adapter operands of one launch from the caller's adapters.
-template <int BN>
-ivit_status encode_lora(const GemmArgs& a, const LoraGemm* lg, LoraOperands<true>* lo) {
-  const uint64_t R = (uint64_t)lg->R;
-  ivit_status st = encode_tmap_3d_u8(&lo->T, lg->T, R, lg->rows, (uint64_t)a.M / lg->rows, kLoraChunk, BN,
-                                     CU_TENSOR_MAP_SWIZZLE_32B);
-  if (st != IVIT_OK) return st;
-  st = encode_tmap_3d_u8(&lo->B, lg->B, R, (uint64_t)a.N, (uint64_t)lg->n, kLoraChunk, kBM, CU_TENSOR_MAP_SWIZZLE_32B);
-  lo->idx = lg->idx;
-  lo->rows = (uint32_t)lg->rows;
-  lo->n = lg->n;
-  lo->chunks = (lg->R + kLoraChunk - 1) / kLoraChunk;
-  return st;
-}
-template <int BN>
-ivit_status encode_lora(const GemmArgs&, const LoraGemm*, LoraOperands<false>*) {
-  return IVIT_OK;
+template <int LORA>
+LoraArgs<LORA> lora_args(const LoraGemm* lg) {
+  if constexpr (LORA != kLoraNone)
+    return LoraArgs<LORA>{lg->T, lg->B, lg->idx, (uint32_t)lg->rows, lg->n, lg->R};
+  else
+    return LoraArgs<LORA>{};
 }
 
-template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
+template <int BN, int STAGES, int EPI, bool NARROW, int LORA>
 ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                          const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
   using L = OwnLayout<BN, STAGES>;
@@ -1106,23 +1182,24 @@ ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, 
   } else {
     tmS = tmY;  // unused
   }
-  LoraOperands<LORA> lora;
-  if ((st = encode_lora<BN>(a, lg, &lora)) != IVIT_OK) return st;
+  constexpr int kSmem = L::kAlloc + (LORA == kLoraMma ? STAGES * 8 : 0);
+  static_assert(kSmem <= 227 * 1024 && L::kBytes % 8 == 0, "shared memory budget");
   auto kern = gemm_own_kernel<BN, STAGES, EPI, NARROW, LORA>;
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
       return IVIT_ERR_CUDA;
     attr_done[dc.device] = true;
   }
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kGemmThreads), L::kAlloc, stream, tmW, tmX, tmY, tmS, lora, a);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), kSmem, stream, tmW, tmX, tmY, tmS,
+                                   lora_args<LORA>(lg), a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
 
-template <int BN, int STAGES, int EPI, bool NARROW, bool LORA>
+template <int BN, int STAGES, int EPI, bool NARROW, int LORA>
 ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                      const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
   using L = GemmLayout<BN, STAGES>;
@@ -1143,18 +1220,19 @@ ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, cons
   } else {
     tmS = tmY;  // unused
   }
-  LoraOperands<LORA> lora;
-  if ((st = encode_lora<BN>(a, lg, &lora)) != IVIT_OK) return st;
+  constexpr int kSmem = L::kAlloc + (LORA == kLoraMma ? STAGES * 8 : 0);
+  static_assert(kSmem <= 227 * 1024 && L::kBytes % 8 == 0, "shared memory budget");
   auto kern = gemm_i8_requant_kernel<BN, STAGES, EPI, NARROW, LORA>;
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
       return IVIT_ERR_CUDA;
     attr_done[dc.device] = true;
   }
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kGemmThreads), L::kAlloc, stream, tmW, tmX, tmY, tmS, lora, a);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), kSmem, stream, tmW, tmX, tmY, tmS,
+                                   lora_args<LORA>(lg), a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
@@ -1216,32 +1294,40 @@ bool use_own_tiles(int K) {
   return K <= 512 || (EPI == kEpiGelu && K <= 768);
 }
 
-template <int EPI, bool NARROW, bool LORA>
+// How a launch's adapters join the accumulators: per token tile, the MMA way costs
+// with the number of requests, the dp4a way does not.
+LoraKind lora_kind(const LoraGemm& lg, int64_t M) { return lg.rows * 8 >= 128 || M <= lg.rows ? kLoraMma : kLoraEpi; }
+
+template <int EPI, bool NARROW, int LORA>
 ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                         const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
-  if (use_own_tiles<EPI>(a.K)) {
-    switch (pick_bn_own(a.M, a.N, dc.num_sms)) {
-      case 160:
-        return run_gemm_own<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-      case 144:
-        return run_gemm_own<144, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-      default:
-        return run_gemm_own<128, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+  if constexpr (LORA == kLoraEpi) {
+    return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+  } else {
+    if (use_own_tiles<EPI>(a.K)) {
+      switch (pick_bn_own(a.M, a.N, dc.num_sms)) {
+        case 160:
+          return run_gemm_own<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        case 144:
+          return run_gemm_own<144, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        default:
+          return run_gemm_own<128, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      }
     }
-  }
-  switch (pick_bn(a.M, a.N, dc.num_sms)) {
-    case 256:
-      return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    case 224:
-      return run_gemm<224, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    case 192:
-      return run_gemm<192, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    case 176:
-      return run_gemm<176, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    case 160:
-      return run_gemm<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    default:
-      return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+    switch (pick_bn(a.M, a.N, dc.num_sms)) {
+      case 256:
+        return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      case 224:
+        return run_gemm<224, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      case 192:
+        return run_gemm<192, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      case 176:
+        return run_gemm<176, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      case 160:
+        return run_gemm<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      default:
+        return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+    }
   }
 }
 
@@ -1267,9 +1353,11 @@ ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t
   a.status = dc.status;
   a.withhold = take_withhold(kWithholdGemm);
   const bool narrow = out_bits < 8;
-#define IVIT_GEMM_DISPATCH(EPI, NARROW)                                              \
-  (lora ? dispatch_bn<EPI, NARROW, true>(dc, X, W, skip, Y, a, lora, stream)         \
-        : dispatch_bn<EPI, NARROW, false>(dc, X, W, skip, Y, a, nullptr, stream))
+  const LoraKind kind = lora ? lora_kind(*lora, M) : kLoraNone;
+#define IVIT_GEMM_DISPATCH(EPI, NARROW)                                                            \
+  (kind == kLoraNone  ? dispatch_bn<EPI, NARROW, kLoraNone>(dc, X, W, skip, Y, a, nullptr, stream) \
+   : kind == kLoraMma ? dispatch_bn<EPI, NARROW, kLoraMma>(dc, X, W, skip, Y, a, lora, stream)     \
+                      : dispatch_bn<EPI, NARROW, kLoraEpi>(dc, X, W, skip, Y, a, lora, stream))
   switch (mode) {
     case kEpiPlain:
       return narrow ? IVIT_GEMM_DISPATCH(kEpiPlain, true) : IVIT_GEMM_DISPATCH(kEpiPlain, false);
