@@ -109,6 +109,11 @@ struct LoraArgs {
 template <>
 struct LoraArgs<kLoraNone> {};
 
+// stages of the adapters' own: two where shared memory has room for them
+template <int BN, int LORA>
+constexpr int lora_stages() {
+  return LORA == kLoraMma ? (BN <= 128 ? 2 : 1) : 0;
+}
 template <int LORA>
 constexpr int gemm_threads() {
   return kGemmThreads + (LORA == kLoraMma ? 32 : 0);
@@ -125,18 +130,6 @@ IVIT_DEV void lora_span(const LoraArgs<kLoraMma>& lo, int64_t M, int tb, uint32_
 }
 constexpr int kPiecesPerStage = kBK / 16;
 
-// k-slices of a tile, the adapters' included, and the MMA steps of 32 bytes in slice kb
-template <int BN, int LORA>
-IVIT_DEV int tile_slices(const LoraArgs<LORA>& lo, int64_t M, int tb, int num_kb, int& pieces) {
-  pieces = 0;
-  if constexpr (LORA == kLoraMma) {
-    uint32_t q0;
-    lora_span<BN>(lo, M, tb, q0, pieces);
-    return num_kb + (pieces + kPiecesPerStage - 1) / kPiecesPerStage;
-  }
-  return num_kb;
-}
-
 IVIT_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
@@ -148,30 +141,25 @@ IVIT_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
 // B's half of it holds is then multiplied by zero), and so does a request
 // without an adapter.
 //
-// The TMA warp, which alone goes through the ring slice by slice, waits until a
-// stage is empty and hands it over through grant[stage]: a wait on `empty` from
-// here could be whole phases ahead or behind, which a parity cannot tell.  A
-// stage is granted again only after its last filling has been consumed, so each
-// grant barrier is at most one phase ahead of the parity kept here.
-template <int BN, int STAGES, int kABytes, int kStageBytes>
-IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int num_kb, int ch_tiles, int num_tiles,
-                        uint8_t* smem, uint64_t* full, uint64_t* grant, int* status) {
+// The stages are the adapters' own (XS of them besides the ring), so a tile's
+// are filled while its k-slices are multiplied.  (Filled in ring order they had
+// only the ring's depth of time: ViT-L fc1 41.9 us.)
+template <int BN, int XS, int kABytes, int kStageBytes>
+IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_tiles, int num_tiles, uint8_t* stages,
+                        uint64_t* full, uint64_t* empty, int* status) {
   const int lane = threadIdx.x & 31;
   const int P = lo.R / 16;
-  uint32_t pos = 0;   // slices of this CTA's sequence so far
-  uint32_t used = 0;  // bit s: parity of stage s's grants so far
+  uint32_t m = 0;  // adapter slices of this CTA so far
   for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
     const int cb = t % ch_tiles, tb = t / ch_tiles;
     const int64_t tok0 = (int64_t)tb * BN;
     uint32_t q0;
     int pieces;
     lora_span<BN>(lo, M, tb, q0, pieces);
-    pos += (uint32_t)num_kb;
-    for (int u0 = 0; u0 < pieces; u0 += kPiecesPerStage, ++pos) {
-      const int stage = (int)(pos % STAGES);
-      if (!__all_sync(0xffffffffu, mbar_wait(&grant[stage], (used >> stage) & 1u, status))) return;
-      used ^= 1u << stage;
-      const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+    for (int u0 = 0; u0 < pieces; u0 += kPiecesPerStage, ++m) {
+      const int stage = (int)(m % XS);
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], ((m / XS) & 1u) ^ 1u, status))) return;
+      const uint32_t sa = smem_u32(stages + stage * kStageBytes), sb = sa + kABytes;
       const int np = min(kPiecesPerStage, pieces - u0);
       for (int i = 0; i < ((np + 1) & ~1); ++i) {
         const int r = (u0 + i) / P, part = (u0 + i) - r * P;
@@ -227,7 +215,8 @@ IVIT_DEV void lora_add(uint32_t (&r)[16], const LoraArgs<kLoraEpi>& lo, int64_t 
   }
 }
 
-template <int BN, int STAGES>
+// XS: stages of the adapters' own, after the ring
+template <int BN, int STAGES, int XS>
 struct GemmLayout {
   // MMA-issuing threads: two when each can own half of the ring's stages
   static constexpr int kIssuers = (STAGES % 2 == 0) ? 2 : 1;
@@ -236,16 +225,18 @@ struct GemmLayout {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kChunks = BN / 16;
   static constexpr int kMaxPart = (kChunks + kEpiParts - 1) / kEpiParts;  // chunks of the largest part
-  static constexpr int kOutOff = STAGES * kStageBytes;
+  static constexpr int kLoraOff = STAGES * kStageBytes;
+  static constexpr int kOutOff = (STAGES + XS) * kStageBytes;
   static constexpr int kPartSlots = kMaxPart * kSlotBytes;  // 1024-byte aligned, as the swizzle needs
   static constexpr int kSetBytes = kEpiParts * kPartSlots;    // one slot set: every part's chunks
   // Two slot sets, used by alternate tiles, when they fit: a tile's stores
   // then have a whole tile's time to finish reading their slots.
-  static constexpr int kFixedBytes = (2 * STAGES + 5 + kEpiParts) * 8 + 16 + 256 + 1024;
+  static constexpr int kFixedBytes = (2 * STAGES + 5 + kEpiParts + 2 * XS) * 8 + 16 + 256 + 1024;
   static constexpr int kSlotSets = (kOutOff + 2 * kSetBytes + kFixedBytes <= 227 * 1024) ? 2 : 1;
   static constexpr int kBarOff = kOutOff + kSlotSets * kSetBytes;
-  // full, empty (STAGES each), tmem full x2, tmem empty x2, drain, one skip barrier per part
-  static constexpr int kNumBars = 2 * STAGES + 5 + kEpiParts;
+  // full, empty (STAGES each), tmem full x2, tmem empty x2, drain, one skip barrier per part,
+  // the adapter stages' full and empty
+  static constexpr int kNumBars = 2 * STAGES + 5 + kEpiParts + 2 * XS;
   static constexpr int kSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kGeluOff = kSlotOff + 16;
   static constexpr int kBytes = kGeluOff + 256;
@@ -501,7 +492,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     gemm_i8_requant_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                            const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS,
                            const __grid_constant__ LoraArgs<LORA> lora, const GemmArgs args) {
-  using L = GemmLayout<BN, STAGES>;
+  using L = GemmLayout<BN, STAGES, lora_stages<BN, LORA>()>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -512,7 +503,9 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   uint64_t* skip_full = drain + 1;  // [kEpiParts]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   int8_t* gelu_tab = reinterpret_cast<int8_t*>(smem + L::kGeluOff);
-  [[maybe_unused]] uint64_t* grant = reinterpret_cast<uint64_t*>(smem + L::kBytes);  // [STAGES], kLoraMma only
+  constexpr int XS = lora_stages<BN, LORA>();
+  [[maybe_unused]] uint64_t* lora_full = skip_full + kEpiParts;  // [XS]
+  [[maybe_unused]] uint64_t* lora_empty = lora_full + XS;        // [XS]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -527,7 +520,6 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      if (LORA == kLoraMma) mbar_init(&grant[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], L::kIssuers);  // one commit per issuing thread
@@ -535,6 +527,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     }
     mbar_init(drain, L::kIssuers);
     for (int e = 0; e < kEpiParts; ++e) mbar_init(&skip_full[e], 1);
+    for (int x = 0; x < 2 * XS; ++x) mbar_init(&lora_full[x], 1);  // and lora_empty
     fence_barrier_init();
     prefetch_tensormap(&tmW);
     prefetch_tensormap(&tmX);
@@ -587,17 +580,6 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
             phase ^= 1;
           }
         }
-        if constexpr (LORA == kLoraMma) {  // the adapter stages go to warp 15
-          int pieces;
-          for (int kb = tile_slices<BN, LORA>(lora, M, tb, num_kb, pieces); kb > num_kb && ok; --kb) {
-            ok = mbar_wait(&empty[stage], phase ^ 1, args.status);
-            if (ok) mbar_arrive(&grant[stage]);
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1;
-            }
-          }
-        }
       }
     }
   } else if (warp <= 2) {
@@ -618,16 +600,15 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
       int kb0 = warp - 1;  // this thread's first k-slice within the current tile
       int acc = 0;
       uint32_t acc_phase = 0;
+      [[maybe_unused]] uint32_t lora_n = 0;  // adapter slices so far
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         // the buffer holds this tile's bias once the epilogue has drained it
         if (!mbar_wait(&tempty[acc], acc_phase, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * L::kAccCols);
-        [[maybe_unused]] int pieces;
-        const int tile_kb = LORA == kLoraMma ? tile_slices<BN, LORA>(lora, M, t / ch_tiles, num_kb, pieces) : num_kb;
         int kb = kb0;
-        for (; kb < tile_kb; kb += kStep) {
+        for (; kb < num_kb; kb += kStep) {
           if (!mbar_wait(&full[stage], phase, args.status)) {
             ok = false;
             break;
@@ -635,14 +616,9 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
           tc_fence_after();
           const uint32_t a_lo = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
           const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
-          if (LORA == kLoraMma && kb >= num_kb) {
-            const int steps = (min(kPiecesPerStage, pieces - (kb - num_kb) * kPiecesPerStage) + 1) / 2;
-            for (int k = 0; k < steps; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
-          } else {
 #pragma unroll
-            for (int k = 0; k < kBK / 32; ++k)  // accumulate onto the preloaded bias
-              umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
-          }
+          for (int k = 0; k < kBK / 32; ++k)  // accumulate onto the preloaded bias
+            umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
           umma_commit(&empty[stage]);
           stage += kStep;
           if (stage >= STAGES) {
@@ -651,7 +627,26 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
           }
         }
         if (!ok) break;
-        kb0 = kb - tile_kb;
+        kb0 = kb - num_kb;
+        if constexpr (LORA == kLoraMma) {  // the tile's adapter slices: the first issuer's
+          if (warp == 1) {
+            uint32_t q0;
+            int pieces;
+            lora_span<BN>(lora, M, t / ch_tiles, q0, pieces);
+            for (; pieces > 0 && ok; pieces -= kPiecesPerStage, ++lora_n) {
+              const int x = (int)(lora_n % XS);
+              ok = mbar_wait(&lora_full[x], (lora_n / XS) & 1u, args.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t a_lo = d_lo0 + (uint32_t)((L::kLoraOff + x * L::kStageBytes) >> 4);
+              const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
+              const int steps = (min(kPiecesPerStage, pieces) + 1) / 2;
+              for (int k = 0; k < steps; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
+              umma_commit(&lora_empty[x]);
+            }
+          }
+          if (!ok) break;
+        }
         // arrives once this thread's MMAs of the tile (possibly none) are done
         umma_commit(&tfull[acc]);
         acc ^= 1;
@@ -664,8 +659,8 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   } else if (LORA == kLoraMma && warp == 3 + kEpiWarps) {
     // ------------------------------------------------------------ adapter stages
     if constexpr (LORA == kLoraMma)
-      lora_fill<BN, STAGES, L::kABytes, L::kStageBytes>(lora, M, N, num_kb, ch_tiles, num_tiles, smem, full, grant,
-                                                        args.status);
+      lora_fill<BN, XS, L::kABytes, L::kStageBytes>(lora, M, N, ch_tiles, num_tiles, smem + L::kLoraOff, lora_full,
+                                                    lora_empty, args.status);
   } else {
     // ------------------------------------------------------------ epilogue
     constexpr int kChunks = L::kChunks;
@@ -849,19 +844,22 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
 // cycling over three buffers.
 // ---------------------------------------------------------------------------
 constexpr int kOwnAcc = 3;
+constexpr int kOwnBN = 160;  // widest tile; every width keeps one stage for adapters
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, int XS>
 struct OwnLayout {
   static constexpr int kIssuers = (STAGES % 2 == 0) ? 2 : 1;
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kBBytes = BN * kBK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kChunks = BN / 16;
-  static constexpr int kOutOff = STAGES * kStageBytes;
+  static constexpr int kLoraOff = STAGES * kStageBytes;
+  static constexpr int kOutOff = (STAGES + XS) * kStageBytes;
   static constexpr int kPartSlots = kChunks * kSlotBytes;  // a whole tile per part
   static constexpr int kBarOff = kOutOff + kEpiParts * kPartSlots;
-  // full, empty (STAGES each), tmem full / empty (three each), drain, one skip barrier per part
-  static constexpr int kNumBars = 2 * STAGES + 2 * kOwnAcc + 1 + kEpiParts;
+  // full, empty (STAGES each), tmem full / empty (three each), drain, one skip barrier per part,
+  // the adapter stages' full and empty
+  static constexpr int kNumBars = 2 * STAGES + 2 * kOwnAcc + 1 + kEpiParts + 2 * XS;
   static constexpr int kSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kGeluOff = kSlotOff + 16;
   static constexpr int kBytes = kGeluOff + 256;
@@ -876,7 +874,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     gemm_own_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS,
                     const __grid_constant__ LoraArgs<LORA> lora, const GemmArgs args) {
-  using L = OwnLayout<BN, STAGES>;
+  using L = OwnLayout<BN, STAGES, lora_stages<kOwnBN, LORA>()>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -887,7 +885,9 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   uint64_t* skip_full = drain + 1;       // [kEpiParts]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   int8_t* gelu_tab = reinterpret_cast<int8_t*>(smem + L::kGeluOff);
-  [[maybe_unused]] uint64_t* grant = reinterpret_cast<uint64_t*>(smem + L::kBytes);  // [STAGES], kLoraMma only
+  constexpr int XS = lora_stages<kOwnBN, LORA>();
+  [[maybe_unused]] uint64_t* lora_full = skip_full + kEpiParts;  // [XS]
+  [[maybe_unused]] uint64_t* lora_empty = lora_full + XS;        // [XS]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -902,7 +902,6 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      if (LORA == kLoraMma) mbar_init(&grant[s], 1);
     }
     for (int a = 0; a < kOwnAcc; ++a) {
       mbar_init(&tfull[a], L::kIssuers);  // one commit per issuing thread
@@ -910,6 +909,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     }
     mbar_init(drain, L::kIssuers);
     for (int e = 0; e < kEpiParts; ++e) mbar_init(&skip_full[e], 1);
+    for (int x = 0; x < 2 * XS; ++x) mbar_init(&lora_full[x], 1);  // and lora_empty
     fence_barrier_init();
     prefetch_tensormap(&tmW);
     prefetch_tensormap(&tmX);
@@ -960,17 +960,6 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
             phase ^= 1;
           }
         }
-        if constexpr (LORA == kLoraMma) {  // the adapter stages go to warp 15
-          int pieces;
-          for (int kb = tile_slices<BN, LORA>(lora, M, tb, num_kb, pieces); kb > num_kb && ok; --kb) {
-            ok = mbar_wait(&empty[stage], phase ^ 1, args.status);
-            if (ok) mbar_arrive(&grant[stage]);
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1;
-            }
-          }
-        }
       }
     }
   } else if (warp <= 2) {
@@ -985,15 +974,14 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
       int kb0 = warp - 1;
       int acc = 0;
       uint32_t acc_phase = 0;
+      [[maybe_unused]] uint32_t lora_n = 0;  // adapter slices so far
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         if (!mbar_wait(&tempty[acc], acc_phase, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * L::kAccCols);
-        [[maybe_unused]] int pieces;
-        const int tile_kb = LORA == kLoraMma ? tile_slices<BN, LORA>(lora, M, t / ch_tiles, num_kb, pieces) : num_kb;
         int kb = kb0;
-        for (; kb < tile_kb; kb += kStep) {
+        for (; kb < num_kb; kb += kStep) {
           if (!mbar_wait(&full[stage], phase, args.status)) {
             ok = false;
             break;
@@ -1001,13 +989,8 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
           tc_fence_after();
           const uint32_t a_lo = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
           const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
-          if (LORA == kLoraMma && kb >= num_kb) {
-            const int steps = (min(kPiecesPerStage, pieces - (kb - num_kb) * kPiecesPerStage) + 1) / 2;
-            for (int k = 0; k < steps; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
-          } else {
 #pragma unroll
-            for (int k = 0; k < kBK / 32; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
-          }
+          for (int k = 0; k < kBK / 32; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
           umma_commit(&empty[stage]);
           stage += kStep;
           if (stage >= STAGES) {
@@ -1016,7 +999,26 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
           }
         }
         if (!ok) break;
-        kb0 = kb - tile_kb;
+        kb0 = kb - num_kb;
+        if constexpr (LORA == kLoraMma) {  // the tile's adapter slices: the first issuer's
+          if (warp == 1) {
+            uint32_t q0;
+            int pieces;
+            lora_span<BN>(lora, M, t / ch_tiles, q0, pieces);
+            for (; pieces > 0 && ok; pieces -= kPiecesPerStage, ++lora_n) {
+              const int x = (int)(lora_n % XS);
+              ok = mbar_wait(&lora_full[x], (lora_n / XS) & 1u, args.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t a_lo = d_lo0 + (uint32_t)((L::kLoraOff + x * L::kStageBytes) >> 4);
+              const uint32_t b_lo = a_lo + (uint32_t)(L::kABytes >> 4);
+              const int steps = (min(kPiecesPerStage, pieces) + 1) / 2;
+              for (int k = 0; k < steps; ++k) umma_i8_acc(d_tmem, a_lo + 2 * k, d_hi, b_lo + 2 * k, d_hi, idesc);
+              umma_commit(&lora_empty[x]);
+            }
+          }
+          if (!ok) break;
+        }
         umma_commit(&tfull[acc]);
         if (++acc == kOwnAcc) {
           acc = 0;
@@ -1029,8 +1031,8 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   } else if (LORA == kLoraMma && warp == 3 + kEpiWarps) {
     // ------------------------------------------------------------ adapter stages
     if constexpr (LORA == kLoraMma)
-      lora_fill<BN, STAGES, L::kABytes, L::kStageBytes>(lora, M, N, num_kb, ch_tiles, num_tiles, smem, full, grant,
-                                                        args.status);
+      lora_fill<BN, XS, L::kABytes, L::kStageBytes>(lora, M, N, ch_tiles, num_tiles, smem + L::kLoraOff, lora_full,
+                                                    lora_empty, args.status);
   } else {
     // ------------------------------------------------------------ epilogue
     constexpr int kChunks = L::kChunks;
@@ -1166,7 +1168,7 @@ LoraArgs<LORA> lora_args(const LoraGemm* lg) {
 template <int BN, int STAGES, int EPI, bool NARROW, int LORA>
 ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                          const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
-  using L = OwnLayout<BN, STAGES>;
+  using L = OwnLayout<BN, STAGES, lora_stages<kOwnBN, LORA>()>;
   CUtensorMap tmW, tmX, tmY, tmS;
   ivit_status st = encode_tmap_2d_u8(&tmW, W, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.K, kBK, kBM,
                                      CU_TENSOR_MAP_SWIZZLE_128B);
@@ -1182,18 +1184,16 @@ ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, 
   } else {
     tmS = tmY;  // unused
   }
-  constexpr int kSmem = L::kAlloc + (LORA == kLoraMma ? STAGES * 8 : 0);
-  static_assert(kSmem <= 227 * 1024 && L::kBytes % 8 == 0, "shared memory budget");
   auto kern = gemm_own_kernel<BN, STAGES, EPI, NARROW, LORA>;
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
       return IVIT_ERR_CUDA;
     attr_done[dc.device] = true;
   }
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), kSmem, stream, tmW, tmX, tmY, tmS,
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), L::kAlloc, stream, tmW, tmX, tmY, tmS,
                                    lora_args<LORA>(lg), a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
@@ -1202,7 +1202,7 @@ ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, 
 template <int BN, int STAGES, int EPI, bool NARROW, int LORA>
 ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                      const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
-  using L = GemmLayout<BN, STAGES>;
+  using L = GemmLayout<BN, STAGES, lora_stages<BN, LORA>()>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory budget");
   CUtensorMap tmW, tmX, tmY, tmS;
   ivit_status st = encode_tmap_2d_u8(&tmW, W, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.K, kBK, kBM,
@@ -1220,18 +1220,16 @@ ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, cons
   } else {
     tmS = tmY;  // unused
   }
-  constexpr int kSmem = L::kAlloc + (LORA == kLoraMma ? STAGES * 8 : 0);
-  static_assert(kSmem <= 227 * 1024 && L::kBytes % 8 == 0, "shared memory budget");
   auto kern = gemm_i8_requant_kernel<BN, STAGES, EPI, NARROW, LORA>;
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
       return IVIT_ERR_CUDA;
     attr_done[dc.device] = true;
   }
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), kSmem, stream, tmW, tmX, tmY, tmS,
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), L::kAlloc, stream, tmW, tmX, tmY, tmS,
                                    lora_args<LORA>(lg), a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
@@ -1246,12 +1244,13 @@ ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, cons
 // two constants are fitted to per-kernel timings of the ViT-B, ViT-L,
 // DeiT-S and ViT-B/384 layers on a B200 (148 SMs), where they reproduce
 // every measured preference between widths.
-int pick_bn(int64_t M, int N, int num_sms) {
+int pick_bn(int64_t M, int N, int num_sms, int widest) {
   static const int cands[] = {256, 224, 192, 176, 160, 128};
   const int ch_tiles = (N + kBM - 1) / kBM;
   int best = 256;
   int64_t best_cost = INT64_MAX;
   for (int bn : cands) {
+    if (bn > widest) continue;
     const int64_t tiles = (int64_t)ch_tiles * ((M + bn - 1) / bn);
     const int64_t rounds = (tiles + num_sms - 1) / num_sms;
     const int64_t cost = rounds * (bn + 112 + (bn == 256 ? 20 : 0));
@@ -1304,29 +1303,32 @@ ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, c
   if constexpr (LORA == kLoraEpi) {
     return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
   } else {
+    // ring depths: the adapters' own stages come out of the ring
+    constexpr int kLess = lora_stages<224, LORA>();
     if (use_own_tiles<EPI>(a.K)) {
       switch (pick_bn_own(a.M, a.N, dc.num_sms)) {
         case 160:
-          return run_gemm_own<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+          return run_gemm_own<160, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
         case 144:
-          return run_gemm_own<144, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+          return run_gemm_own<144, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
         default:
           return run_gemm_own<128, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       }
     }
-    switch (pick_bn(a.M, a.N, dc.num_sms)) {
+    switch (pick_bn(a.M, a.N, dc.num_sms, LORA == kLoraNone ? 256 : 224)) {
       case 256:
-        return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        if constexpr (LORA == kLoraNone) return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        [[fallthrough]];
       case 224:
-        return run_gemm<224, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<224, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 192:
-        return run_gemm<192, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<192, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 176:
-        return run_gemm<176, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<176, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 160:
-        return run_gemm<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<160, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       default:
-        return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<128, 6 - 2 * kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     }
   }
 }
