@@ -66,6 +66,10 @@
 //              with 16-byte cp.async, whose source size of zero writes zeros;
 //   kLoraEpi   requests of few tokens, where the axis would be mostly zeros:
 //              the epilogue warps add t . B_a to the accumulators with dp4a.
+// Only the warps that read t wait for the kernel before them (pdl_wait): that
+// kernel has itself waited for all earlier ones before it lets this one start,
+// and writes nothing but t, so X, W and the skip tensor are read and the
+// k-slices multiplied while it runs.
 #include <climits>
 
 #include "ivit_common.cuh"
@@ -149,6 +153,8 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
                         uint64_t* full, uint64_t* empty, int* status) {
   const int lane = threadIdx.x & 31;
   const int P = lo.R / 16;
+  pdl_wait();  // t comes from the kernel before
+  pdl_launch_dependents();
   uint32_t m = 0;  // adapter slices of this CTA so far
   for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
     const int cb = t % ch_tiles, tb = t / ch_tiles;
@@ -548,8 +554,10 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tslot;
-  pdl_wait();  // X, the skip tensor and t come from earlier kernels
-  pdl_launch_dependents();
+  if (LORA == kLoraNone) {
+    pdl_wait();  // X and the skip tensor come from earlier kernels
+    pdl_launch_dependents();
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -684,6 +692,10 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
       const int ch = (t % ch_tiles) * kBM + quarter * 32 + lane;
       return (args.bias && ch < N) ? __ldg(args.bias + ch) : 0;
     };
+    if (LORA == kLoraEpi) {
+      pdl_wait();  // t comes from the kernel before
+      pdl_launch_dependents();
+    }
     // both accumulator buffers start out holding the bias of their first tile
     for (int a = 0; a < 2; ++a) {
       const int t = (int)blockIdx.x + a * (int)gridDim.x;
@@ -930,8 +942,10 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tslot;
-  pdl_wait();  // X, the skip tensor and t come from earlier kernels
-  pdl_launch_dependents();
+  if (LORA == kLoraNone) {
+    pdl_wait();  // X and the skip tensor come from earlier kernels
+    pdl_launch_dependents();
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -1301,34 +1315,42 @@ template <int EPI, bool NARROW, int LORA>
 ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                         const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
   if constexpr (LORA == kLoraEpi) {
+    // the adapters' part is spread over the SMs as far as the tokens go: the
+    // narrowest tiles (one chunk of tokens, one per epilogue part) that still fit in one round
+    const int64_t ch_tiles = (a.N + kBM - 1) / kBM;
+    if (ch_tiles * ((a.M + 15) / 16) <= dc.num_sms)
+      return run_gemm<16, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+    if (ch_tiles * ((a.M + 47) / 48) <= dc.num_sms)
+      return run_gemm<48, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
   } else {
-    // ring depths: the adapters' own stages come out of the ring
-    constexpr int kLess = lora_stages<224, LORA>();
+    // ring depths: where the adapters' own stages do not fit beside it, the ring
+    // is three deep (one MMA issuer), which the widest tiles bear best
+    constexpr bool kPlain = LORA == kLoraNone;
     if (use_own_tiles<EPI>(a.K)) {
       switch (pick_bn_own(a.M, a.N, dc.num_sms)) {
         case 160:
-          return run_gemm_own<160, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+          return run_gemm_own<160, kPlain ? 4 : 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
         case 144:
-          return run_gemm_own<144, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+          return run_gemm_own<144, kPlain ? 4 : 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
         default:
           return run_gemm_own<128, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       }
     }
-    switch (pick_bn(a.M, a.N, dc.num_sms, LORA == kLoraNone ? 256 : 224)) {
+    switch (pick_bn(a.M, a.N, dc.num_sms, kPlain ? 256 : 224)) {
       case 256:
-        if constexpr (LORA == kLoraNone) return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        if constexpr (kPlain) return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
         [[fallthrough]];
       case 224:
-        return run_gemm<224, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<224, kPlain ? 4 : 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 192:
-        return run_gemm<192, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<192, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 176:
-        return run_gemm<176, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<176, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 160:
-        return run_gemm<160, 4 - kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<160, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       default:
-        return run_gemm<128, 6 - 2 * kLess, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        return run_gemm<128, kPlain ? 6 : 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     }
   }
 }
