@@ -1324,8 +1324,8 @@ ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, c
       return run_gemm<48, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
   } else {
-    // ring depths: where the adapters' own stages do not fit beside it, the ring
-    // is three deep (one MMA issuer), which the widest tiles bear best
+    // beside adapters at most 192 tokens a tile: a ring of four (two MMA issuers) and
+    // the adapters' stage fit there (ViT-B QKV 25.5 us; 27.7 with 224 and a ring of three)
     constexpr bool kPlain = LORA == kLoraNone;
     if (use_own_tiles<EPI>(a.K)) {
       switch (pick_bn_own(a.M, a.N, dc.num_sms)) {
@@ -1337,12 +1337,13 @@ ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, c
           return run_gemm_own<128, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       }
     }
-    switch (pick_bn(a.M, a.N, dc.num_sms, kPlain ? 256 : 224)) {
+    switch (pick_bn(a.M, a.N, dc.num_sms, kPlain ? 256 : 192)) {
       case 256:
         if constexpr (kPlain) return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
         [[fallthrough]];
       case 224:
-        return run_gemm<224, kPlain ? 4 : 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        if constexpr (kPlain) return run_gemm<224, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+        [[fallthrough]];
       case 192:
         return run_gemm<192, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       case 176:

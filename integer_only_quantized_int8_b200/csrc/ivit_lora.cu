@@ -15,8 +15,7 @@
 //     and commit, so four threads take the slices in turn, each onto an
 //     accumulator of its own (the epilogue adds them): 6 slices took 1.5 us of a
 //     3.5 us kernel with one;
-//   - tiles hold fewer tokens (64 or 32 rows of the 128) while there are SMs to
-//     take more of them.  Splitting K over a cluster instead, with the partial
+//   - tiles hold fewer than 128 tokens while there are SMs to take more of them.  Splitting K over a cluster instead, with the partial
 //     sums through distributed shared memory, cost 4-6 us after the last MMA;
 //   - the requant is one mul.hi when every multiplier of the adapter is below one
 //     half, as in the GEMM.
@@ -31,7 +30,7 @@ namespace {
 constexpr int kIssuers = 4;        // MMA-issuing warps, an accumulator each
 constexpr int kDownEpiWarps = 8;   // two per TMEM lane quarter
 constexpr int kDownThreads = 32 * (1 + kIssuers + kDownEpiWarps);
-constexpr int kDownRows = 128;     // TMEM lanes of a tile; it may use the first 64 or 32 only
+constexpr int kDownRows = 128;     // TMEM lanes of a tile; it may use the first few only
 constexpr int kDownSlice = 128;    // bytes of K per stage
 constexpr int kDownMaxStages = 16;
 constexpr int kDownSmem = 200 * 1024;  // at most, the ring as deep as that allows
@@ -235,9 +234,10 @@ ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, in
                              const int32_t* b_t, const int8_t* c_t, bool round, const LoraGemm& lora, int8_t* T,
                              cudaStream_t stream) {
   const int64_t requests = M / lora.rows;
-  // the shortest tiles that still go round once
-  int tile_rows = kDownRows;
-  while (tile_rows > 32 && requests * ((lora.rows + tile_rows / 2 - 1) / (tile_rows / 2)) <= dc.num_sms) tile_rows /= 2;
+  // as many tiles of equal height (a multiple of the swizzle's eight rows) as still go round once
+  int64_t per_request = requests < dc.num_sms ? dc.num_sms / requests : 1;
+  if (per_request < (lora.rows + kDownRows - 1) / kDownRows) per_request = (lora.rows + kDownRows - 1) / kDownRows;
+  const int tile_rows = (int)(((lora.rows + per_request - 1) / per_request + 7) / 8 * 8);
   const int64_t tiles = (lora.rows + tile_rows - 1) / tile_rows;  // tiles * requests <= M < 2^31
   CUtensorMap tmX, tmA;
   ivit_status st = encode_tmap_3d_u8(&tmX, X, (uint64_t)K, (uint64_t)lora.rows, (uint64_t)requests, kDownSlice,
@@ -260,8 +260,13 @@ ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, in
       return IVIT_ERR_CUDA;
     attr_done[dc.device] = true;
   }
-  const cudaError_t e = launch_pdl(lora_down_kernel, dim3((unsigned)(tiles * requests)), dim3(kDownThreads),
-                                   (size_t)(stages * stage + fixed), stream, tmX, tmA, a);
+  // Up to one tile per SM is kept to one CTA per SM (more than half its shared
+  // memory): two on the SMs that the kernel before leaves first start the GEMM's
+  // equal shares there late (ViT-L fc1 34.5 us instead of 31.9).
+  int smem = stages * stage + fixed;
+  if (tiles * requests <= dc.num_sms && smem < 116 * 1024) smem = 116 * 1024;
+  const cudaError_t e = launch_pdl(lora_down_kernel, dim3((unsigned)(tiles * requests)), dim3(kDownThreads), (size_t)smem,
+                                   stream, tmX, tmA, a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
