@@ -62,8 +62,8 @@
 //              in other requests' columns).  That layout is in no tensor, and
 //              boxes of R bytes cost TMA as much per row as 128-byte ones (as
 //              tensor maps per request, zero-filled past its rows, the slices
-//              took 8 us of a 27 us ViT-B QKV), so warp 15 fills these stages
-//              with 16-byte cp.async, whose source size of zero writes zeros;
+//              took 8 us of a 27 us ViT-B QKV), so two more warps (lora_fill) fill these
+//              stages with 16-byte cp.async, whose source size of zero writes zeros;
 //   kLoraEpi   requests of few tokens, where the axis would be mostly zeros:
 //              the epilogue warps add t . B_a to the accumulators with dp4a.
 // Only the warps that read t wait for the kernel before them (pdl_wait): that
@@ -113,6 +113,7 @@ struct LoraArgs {
 template <>
 struct LoraArgs<kLoraNone> {};
 
+constexpr int kFillWarps = 2;  // warps that fill the adapters' stages
 // stages of the adapters' own: two where shared memory has room for them
 template <int BN, int LORA>
 constexpr int lora_stages() {
@@ -120,7 +121,7 @@ constexpr int lora_stages() {
 }
 template <int LORA>
 constexpr int gemm_threads() {
-  return kGemmThreads + (LORA == kLoraMma ? 32 : 0);
+  return kGemmThreads + (LORA == kLoraMma ? 32 * kFillWarps : 0);
 }
 
 // First request of the token tile [tb BN, ...) and the 16-byte pieces of its
@@ -138,7 +139,7 @@ IVIT_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 
-// Warp 15: the adapter stages of every tile of this CTA.  Piece u of the axis is
+// The filling warps: the adapter stages of every tile of this CTA.  Piece u of the axis is
 // rank entries [16 (u % P), + 16) of request q0 + u / P, P = R / 16; both
 // operands' rows are 128 bytes, 128B-swizzled, as TMA would leave them.  A last
 // odd piece gets a partner of zeros in t (an MMA step takes 32 bytes; whatever
@@ -152,6 +153,8 @@ template <int BN, int XS, int kABytes, int kStageBytes>
 IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_tiles, int num_tiles, uint8_t* stages,
                         uint64_t* full, uint64_t* empty, int* status) {
   const int lane = threadIdx.x & 31;
+  const int l = (int)threadIdx.x - kGemmThreads;  // among the filling warps
+  constexpr int kStep = 32 * kFillWarps;
   const int P = lo.R / 16;
   pdl_wait();  // t comes from the kernel before
   pdl_launch_dependents();
@@ -173,21 +176,21 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
         const int32_t a = i < np ? __ldg(lo.idx + q) : -1;
         const bool has = a >= 0 && a < lo.n;
         if (has) {
-          const int8_t* b = lo.B + ((int64_t)a * N + cb * kBM + lane) * lo.R + 16 * part;
+          const int8_t* b = lo.B + ((int64_t)a * N + cb * kBM + l) * lo.R + 16 * part;
 #pragma unroll
-          for (int k = 0; k < kBM / 32; ++k) {
-            const int ch = lane + 32 * k;
+          for (int k = 0; k < kBM / kStep; ++k) {
+            const int ch = l + kStep * k;
             if (cb * kBM + ch < N)
-              cp_async16_zfill(sa + (uint32_t)(ch * kBK + ((i ^ (ch & 7)) << 4)), b + (int64_t)(32 * k) * lo.R, true);
+              cp_async16_zfill(sa + (uint32_t)(ch * kBK + ((i ^ (ch & 7)) << 4)), b + (int64_t)(kStep * k) * lo.R, true);
           }
         }
         // the request's rows within the tile
         const int lo_row = (int)(q * lo.rows - tok0), hi_row = lo_row + (int)lo.rows;
 #pragma unroll
-        for (int k = 0; k < (BN + 31) / 32; ++k) {
-          const int row = lane + 32 * k;
+        for (int k = 0; k < (BN + kStep - 1) / kStep; ++k) {
+          const int row = l + kStep * k;
           const bool take = has && row >= lo_row && row < hi_row;
-          if (BN % 32 == 0 || row < BN)
+          if (BN % kStep == 0 || row < BN)
             cp_async16_zfill(sb + (uint32_t)(row * kBK + ((i ^ (row & 7)) << 4)),
                              lo.T + (take ? (tok0 + row) * lo.R + 16 * part : 0), take);
         }
@@ -533,7 +536,10 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     }
     mbar_init(drain, L::kIssuers);
     for (int e = 0; e < kEpiParts; ++e) mbar_init(&skip_full[e], 1);
-    for (int x = 0; x < 2 * XS; ++x) mbar_init(&lora_full[x], 1);  // and lora_empty
+    for (int x = 0; x < XS; ++x) {
+      mbar_init(&lora_full[x], kFillWarps);
+      mbar_init(&lora_empty[x], 1);
+    }
     fence_barrier_init();
     prefetch_tensormap(&tmW);
     prefetch_tensormap(&tmX);
@@ -664,7 +670,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
       umma_commit(drain);
       mbar_wait(drain, 0, args.status);
     }
-  } else if (LORA == kLoraMma && warp == 3 + kEpiWarps) {
+  } else if (LORA == kLoraMma && warp >= 3 + kEpiWarps) {
     // ------------------------------------------------------------ adapter stages
     if constexpr (LORA == kLoraMma)
       lora_fill<BN, XS, L::kABytes, L::kStageBytes>(lora, M, N, ch_tiles, num_tiles, smem + L::kLoraOff, lora_full,
@@ -921,7 +927,10 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
     }
     mbar_init(drain, L::kIssuers);
     for (int e = 0; e < kEpiParts; ++e) mbar_init(&skip_full[e], 1);
-    for (int x = 0; x < 2 * XS; ++x) mbar_init(&lora_full[x], 1);  // and lora_empty
+    for (int x = 0; x < XS; ++x) {
+      mbar_init(&lora_full[x], kFillWarps);
+      mbar_init(&lora_empty[x], 1);
+    }
     fence_barrier_init();
     prefetch_tensormap(&tmW);
     prefetch_tensormap(&tmX);
@@ -1042,7 +1051,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
       umma_commit(drain);
       mbar_wait(drain, 0, args.status);
     }
-  } else if (LORA == kLoraMma && warp == 3 + kEpiWarps) {
+  } else if (LORA == kLoraMma && warp >= 3 + kEpiWarps) {
     // ------------------------------------------------------------ adapter stages
     if constexpr (LORA == kLoraMma)
       lora_fill<BN, XS, L::kABytes, L::kStageBytes>(lora, M, N, ch_tiles, num_tiles, smem + L::kLoraOff, lora_full,
