@@ -203,6 +203,16 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
   }
 }
 
+// Brings this channel's rows of B for the tokens [tok0, tok0 + n) towards the SM
+// while the accumulator is waited for.
+IVIT_DEV void lora_touch(const LoraArgs<kLoraEpi>& lo, int64_t M, int N, int64_t tok0, int n, int ch) {
+  const int8_t* b0 = lo.B + (int64_t)min(ch, N - 1) * lo.R;
+  for (int i = 0; i < n && tok0 + i < M; ++i) {
+    const int32_t a = __ldg(lo.idx + (uint32_t)(tok0 + i) / lo.rows);
+    if (a >= 0 && a < lo.n) asm volatile("prefetch.global.L1 [%0];" ::"l"(b0 + (int64_t)a * N * lo.R));
+  }
+}
+
 // The epilogue's own adapters: r[i] += t . B_a of token tok0 + i and channel ch.
 IVIT_DEV void lora_add(uint32_t (&r)[16], const LoraArgs<kLoraEpi>& lo, int64_t M, int N, int64_t tok0, int ch) {
   const int lane = threadIdx.x & 31;
@@ -698,10 +708,6 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
       const int ch = (t % ch_tiles) * kBM + quarter * 32 + lane;
       return (args.bias && ch < N) ? __ldg(args.bias + ch) : 0;
     };
-    if (LORA == kLoraEpi) {
-      pdl_wait();  // t comes from the kernel before
-      pdl_launch_dependents();
-    }
     // both accumulator buffers start out holding the bias of their first tile
     for (int a = 0; a < 2; ++a) {
       const int t = (int)blockIdx.x + a * (int)gridDim.x;
@@ -777,6 +783,8 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
             tma_load_2d(slots + i * kSlotBytes, &tmS, tile_ch, (int32_t)(tok_base + 16 * (c_begin + i)), sbar);
         }
       }
+      if constexpr (LORA == kLoraEpi)
+        if (live) lora_touch(lora, M, N, tok_base + 16 * c_begin, 16 * n, tile_ch + quarter * 32 + lane);
       const bool got = mbar_wait(&tfull[acc], acc_phase, args.status);
       // the whole part has its accumulator and free slots, or gives up together
       if (!part_bar_and(part, got)) {
@@ -791,6 +799,10 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
         skip_phase ^= 1;
       }
       tc_fence_after();
+      if (LORA == kLoraEpi && t == (int)blockIdx.x) {
+        pdl_wait();  // t comes from the kernel before
+        pdl_launch_dependents();
+      }
       const uint32_t tbase = tlane + (uint32_t)(acc * L::kAccCols);
 #define IVIT_EPI_TILE(R) \
   epi_tile<EPI, NARROW, R, LORA>(tbase, c_begin, n, kc, args, gelu_tab, slots, ofs_even, ofs_odd, sel2, sel1, lora, \
