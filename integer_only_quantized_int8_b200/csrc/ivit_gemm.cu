@@ -109,6 +109,7 @@ struct LoraArgs {
   const int32_t* idx;  // adapter of each request
   uint32_t rows;       // tokens per request
   int32_t n, R;
+  int32_t by_adapter;  // kLoraMma: the axis runs over the adapters, not the tile's requests
 };
 template <>
 struct LoraArgs<kLoraNone> {};
@@ -124,10 +125,15 @@ constexpr int gemm_threads() {
   return kGemmThreads + (LORA == kLoraMma ? 32 * kFillWarps : 0);
 }
 
-// First request of the token tile [tb BN, ...) and the 16-byte pieces of its
-// adapter axis.
+// First request of the token tile [tb BN, ...) (0 by adapter) and the 16-byte
+// pieces of its axis.
 template <int BN>
 IVIT_DEV void lora_span(const LoraArgs<kLoraMma>& lo, int64_t M, int tb, uint32_t& q0, int& pieces) {
+  if (lo.by_adapter) {
+    q0 = 0;
+    pieces = lo.n * (lo.R / 16);
+    return;
+  }
   const uint32_t first = (uint32_t)tb * (uint32_t)BN;  // M < 2^31
   const uint32_t last = min(first + (uint32_t)BN, (uint32_t)M) - 1u;
   q0 = first / lo.rows;
@@ -140,7 +146,8 @@ IVIT_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
 }
 
 // The filling warps: the adapter stages of every tile of this CTA.  Piece u of the axis is
-// rank entries [16 (u % P), + 16) of request q0 + u / P, P = R / 16; both
+// rank entries [16 (u % P), + 16) of request q0 + u / P (by adapter: of adapter
+// u / P), P = R / 16; both
 // operands' rows are 128 bytes, 128B-swizzled, as TMA would leave them.  A last
 // odd piece gets a partner of zeros in t (an MMA step takes 32 bytes; whatever
 // B's half of it holds is then multiplied by zero), and so does a request
@@ -165,6 +172,14 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
     uint32_t q0;
     int pieces;
     lora_span<BN>(lo, M, tb, q0, pieces);
+    // where on the axis each of this thread's rows lies
+    int key[(BN + kStep - 1) / kStep];
+#pragma unroll
+    for (int k = 0; k < (BN + kStep - 1) / kStep; ++k) {
+      const int64_t tok = tok0 + l + kStep * k;
+      const uint32_t q = (uint32_t)tok / lo.rows;
+      key[k] = tok >= M ? -1 : (lo.by_adapter ? __ldg(lo.idx + q) : (int)(q - q0));
+    }
     for (int u0 = 0; u0 < pieces; u0 += kPiecesPerStage, ++m) {
       const int stage = (int)(m % XS);
       if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], ((m / XS) & 1u) ^ 1u, status))) return;
@@ -172,8 +187,7 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
       const int np = min(kPiecesPerStage, pieces - u0);
       for (int i = 0; i < ((np + 1) & ~1); ++i) {
         const int r = (u0 + i) / P, part = (u0 + i) - r * P;
-        const int64_t q = (int64_t)q0 + r;
-        const int32_t a = i < np ? __ldg(lo.idx + q) : -1;
+        const int32_t a = i >= np ? -1 : (lo.by_adapter ? r : __ldg(lo.idx + (int64_t)q0 + r));
         const bool has = a >= 0 && a < lo.n;
         if (has) {
           const int8_t* b = lo.B + ((int64_t)a * N + cb * kBM + l) * lo.R + 16 * part;
@@ -184,12 +198,10 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
               cp_async16_zfill(sa + (uint32_t)(ch * kBK + ((i ^ (ch & 7)) << 4)), b + (int64_t)(kStep * k) * lo.R, true);
           }
         }
-        // the request's rows within the tile
-        const int lo_row = (int)(q * lo.rows - tok0), hi_row = lo_row + (int)lo.rows;
 #pragma unroll
         for (int k = 0; k < (BN + kStep - 1) / kStep; ++k) {
           const int row = l + kStep * k;
-          const bool take = has && row >= lo_row && row < hi_row;
+          const bool take = has && key[k] == r;
           if (BN % kStep == 0 || row < BN)
             cp_async16_zfill(sb + (uint32_t)(row * kBK + ((i ^ (row & 7)) << 4)),
                              lo.T + (take ? (tok0 + row) * lo.R + 16 * part : 0), take);
@@ -1192,10 +1204,13 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   }
 }
 
+// Entries of a token tile's axis by request (160 tokens stand for every width).
+int64_t lora_requests(const LoraGemm& lg, int64_t M) { return ((M < 160 ? M : 160) - 1) / lg.rows + 2; }
+
 template <int LORA>
-LoraArgs<LORA> lora_args(const LoraGemm* lg) {
+LoraArgs<LORA> lora_args(const LoraGemm* lg, int64_t M) {
   if constexpr (LORA != kLoraNone)
-    return LoraArgs<LORA>{lg->T, lg->B, lg->idx, (uint32_t)lg->rows, lg->n, lg->R};
+    return LoraArgs<LORA>{lg->T, lg->B, lg->idx, (uint32_t)lg->rows, lg->n, lg->R, lg->n < lora_requests(*lg, M) ? 1 : 0};
   else
     return LoraArgs<LORA>{};
 }
@@ -1229,7 +1244,7 @@ ivit_status run_gemm_own(const DeviceCtx& dc, const int8_t* X, const int8_t* W, 
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), L::kAlloc, stream, tmW, tmX, tmY, tmS,
-                                   lora_args<LORA>(lg), a);
+                                   lora_args<LORA>(lg, a.M), a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
@@ -1265,7 +1280,7 @@ ivit_status run_gemm(const DeviceCtx& dc, const int8_t* X, const int8_t* W, cons
   const int tiles = ((a.N + kBM - 1) / kBM) * (int)((a.M + BN - 1) / BN);
   const int grid = tiles < dc.num_sms ? tiles : dc.num_sms;
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(gemm_threads<LORA>()), L::kAlloc, stream, tmW, tmX, tmY, tmS,
-                                   lora_args<LORA>(lg), a);
+                                   lora_args<LORA>(lg, a.M), a);
   note_launch();
   return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
 }
@@ -1328,9 +1343,21 @@ bool use_own_tiles(int K) {
   return K <= 512 || (EPI == kEpiGelu && K <= 768);
 }
 
-// How a launch's adapters join the accumulators: per token tile, the MMA way costs
-// with the number of requests, the dp4a way does not.
-LoraKind lora_kind(const LoraGemm& lg, int64_t M) { return lg.rows * 8 >= 128 || M <= lg.rows ? kLoraMma : kLoraEpi; }
+// Whether kLoraEpi's narrow tiles go round the SMs once.
+bool lora_narrow(int64_t M, int N, int num_sms) { return (int64_t)((N + kBM - 1) / kBM) * ((M + 47) / 48) <= num_sms; }
+
+// How a launch's adapters join the accumulators.  The MMA way costs with the
+// length of the axis, min(requests of a tile, adapters) entries, the dp4a way
+// with the tokens, and much less of it where narrow tiles spread them over idle
+// SMs.  Measured (us, MMA / dp4a): K = 768, N = 2304, R = 16, 512 tokens of
+// requests of 1, 2, 4, 8 tokens: 36.5 / 23.7, 20.7 / 20.9, 13.8 / 20.4, 10.1 / 18.2;
+// 4096 tokens: 188 / 100, 99 / 80, 55 / 70, 33 / 66; 64 tokens (narrow): 19.6 / 8.6,
+// 12.7 / 8.3, 9.5 / 8.2, 7.8 / 8.2; ranks 32 and 64 cross at the same lengths.
+LoraKind lora_kind(const LoraGemm& lg, int64_t M, int N, int num_sms) {
+  const int64_t requests = lora_requests(lg, M);
+  const int64_t entries = lg.n < requests ? lg.n : requests;
+  return entries <= (lora_narrow(M, N, num_sms) ? 9 : 56) ? kLoraMma : kLoraEpi;
+}
 
 template <int EPI, bool NARROW, int LORA>
 ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
@@ -1341,7 +1368,7 @@ ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, c
     const int64_t ch_tiles = (a.N + kBM - 1) / kBM;
     if (ch_tiles * ((a.M + 15) / 16) <= dc.num_sms)
       return run_gemm<16, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    if (ch_tiles * ((a.M + 47) / 48) <= dc.num_sms)
+    if (lora_narrow(a.M, a.N, dc.num_sms))
       return run_gemm<48, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
     return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
   } else {
@@ -1399,7 +1426,7 @@ ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t
   a.status = dc.status;
   a.withhold = take_withhold(kWithholdGemm);
   const bool narrow = out_bits < 8;
-  const LoraKind kind = lora ? lora_kind(*lora, M) : kLoraNone;
+  const LoraKind kind = lora ? lora_kind(*lora, M, N, dc.num_sms) : kLoraNone;
 #define IVIT_GEMM_DISPATCH(EPI, NARROW)                                                            \
   (kind == kLoraNone  ? dispatch_bn<EPI, NARROW, kLoraNone>(dc, X, W, skip, Y, a, nullptr, stream) \
    : kind == kLoraMma ? dispatch_bn<EPI, NARROW, kLoraMma>(dc, X, W, skip, Y, a, lora, stream)     \

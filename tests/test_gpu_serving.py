@@ -429,3 +429,51 @@ def test_adapted_block():
         x, z = host_block(x, z)
     np.testing.assert_array_equal(host(dx), x)
     np.testing.assert_array_equal(host(dz), z)
+
+
+# ---------------------------------------------------------------- the ways adapters join
+
+@pytest.mark.parametrize("req,rows,K,N,R,n", [
+    (700, 2, 64, 2304, 16, 64),      # dp4a on wide tiles: many one- and two-token requests, many adapters
+    (130, 3, 256, 1040, 48, 61),     # dp4a on narrow tiles
+    (40, 1, 128, 272, 128, 37),
+    (900, 1, 144, 1168, 32, 8),      # an axis by adapter: more requests than adapters in a tile
+    (500, 3, 640, 576, 112, 3), (90, 7, 1040, 528, 16, 5),
+    (3, 333, 528, 2064, 96, 2), (12, 21, 96, 4096, 64, 50),   # an axis by request, several slices long
+    (2, 1100, 48, 64, 16, 3),        # a request of several tiles and one that shares its last
+])
+@pytest.mark.parametrize("epi", ["plain", "residual", "gelu"])
+def test_linear_lora_ways(req, rows, K, N, R, n, epi):
+    q = LoraCase(req, rows, K, N, R, n, seed=req + rows + K)
+    y, untouched = guarded((q.M, N))
+    if epi == "gelu":
+        ivit.ivit_linear_lora_shiftgelu(*q.device(), *GELU, y, workspace(q.M, R))
+        want = serving.linear_lora(*q.host(), gelu=GELU)
+    else:
+        res = (1 << 29, (1 << 28) + 77, 30) if epi == "residual" else None
+        skip = q.skip if epi == "residual" else None
+        ivit.ivit_linear_lora(*q.device(), y, workspace(q.M, R), 5, dev(skip), res, rounding=1)
+        want = serving.linear_lora(*q.host(), 5, skip, res, 1)
+    np.testing.assert_array_equal(host(y), want)
+    assert untouched()
+
+
+def test_linear_lora_back_to_back():
+    """Layers in a row on one workspace, each reading what the one before wrote: the GEMM that starts while its down
+    projection runs must see neither's inputs early nor its t late."""
+    r = np.random.default_rng(30)
+    dims = [192, 256, 1024, 192, 768, 192]
+    layers = [LoraCase(9, 50, K, N, 32, 4, seed=40 + i) for i, (K, N) in enumerate(zip(dims, dims[1:]))]
+    x = rng_i8(r, 450, 192)
+    bufs = [dev(x)] + [torch.zeros(450, N, dtype=torch.int8, device="cuda") for N in dims[1:]]
+    ws = workspace(450, 32)
+    d = [q.device() for q in layers]
+    for _ in range(10):
+        for i in range(len(layers)):
+            ivit.ivit_linear_lora(bufs[i], *d[i][1:], bufs[i + 1], ws)
+        bufs[0].copy_(bufs[-1])
+    t = x
+    for _ in range(10):
+        for q in layers:
+            t = serving.linear_lora(t, q.W, q.bias, q.b, q.c, q.adapters, q.idx, q.rows)
+    np.testing.assert_array_equal(host(bufs[-1]), t)
