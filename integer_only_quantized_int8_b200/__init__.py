@@ -1,6 +1,7 @@
 """Integer-only ViT encoder block (I-ViT) on B200: Python binding.
 
-A thin ctypes layer over ``libivit_b200.so`` (the C ABI in ``include/ivit.h``).
+A thin ctypes layer over ``libivit_b200.so`` (the C ABI in ``include/ivit.h``;
+the serving operators' calls are marshalled natively, by ``csrc/binding.cpp``).
 Functions keep the C names and only marshal arguments: torch tensors become
 device pointers, ``stream=None`` becomes torch's current CUDA stream, and a
 non-OK status raises :class:`IvitError`.  Every operator runs in the library's
@@ -12,7 +13,6 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-import struct
 import threading
 
 import torch
@@ -228,31 +228,23 @@ def _holds(n: int, **tensors):
             raise ValueError(f"{name} holds {t.numel()} elements, needs {n}")
 
 
-# The serving operators' calls are short enough for the time spent here to
-# count, so their wrappers take each tensor through one test of everything at
-# once, compare sizes in place, and pass small structures packed as bytes.
-
-def _at(t, dtype, dev, name):
-    """The device pointer of a tensor of the call, on the current device ``dev``; None stays None."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    p = _ptr(t, dtype, name)
-    if t is not None and t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return p
+_calls = None
 
 
-def _device(t, name) -> int:
-    """The current device, which the call's kernels and (without an explicit one) its stream are on."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.get_device() < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return torch._C._cuda_getDevice()
-
-
-def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+def _native():
+    """The native marshalling of the serving operators' calls (csrc/binding.cpp), bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _binding as m
+        except ImportError as e:
+            raise RuntimeError("the native binding is missing: build it with "
+                               "`python -m integer_only_quantized_int8_b200.build`") from e
+        m.bind(*(C.cast(f, C.c_void_p).value for f in (L.ivit_linear_lora, L.ivit_linear_lora_shiftgelu,
+                                                       L.ivit_residual_norm, L.ivit_attention_diff)))
+        _calls = m
+    return _calls
 
 
 def _dy(d) -> Dyadic:
@@ -397,32 +389,8 @@ def ivit_linear_lora_workspace_bytes(M: int, R: int) -> int:
     return int(lib().ivit_linear_lora_workspace_bytes(int(M), int(R)))
 
 
-_pack_lora = struct.Struct("@iiPPPP").pack         # ivit_lora
-_pack_norm = struct.Struct("@PPiiii").pack         # ivit_norm
-_NO_RESIDUAL = Residual(0, 0, 0)
-
-
-def _lora_args(X, W, bias, b, c, adapters, idx, rows, Y, skip=None):
-    """Shape checks shared by the linear layers with adapters: (device, M, K, N, packed ivit_lora)."""
-    M, K = X.shape
-    N, Kw = W.shape
-    A, b_t, c_t, B = adapters
-    n, R = A.shape[:2]
-    if Kw != K or Y.shape != (M, N) or A.shape != (n, R, K) or B.shape != (n, N, R):
-        raise ValueError("shape mismatch")
-    if skip is not None and skip.shape != (M, N):
-        raise ValueError("skip shape mismatch")
-    if rows < 1 or M % rows:
-        raise ValueError(f"shape mismatch: {M} rows are not requests of {rows}")
-    if b.numel() < N or c.numel() < N or (bias is not None and bias.numel() < N):
-        _holds(N, bias=bias, b=b, c=c)
-    if b_t.numel() < n * R or c_t.numel() < n * R:
-        _holds(n * R, b_t=b_t, c_t=c_t)
-    if idx.numel() < M // rows:
-        _holds(M // rows, idx=idx)
-    dev = _device(X, "X")
-    return dev, M, K, N, _pack_lora(n, R, _at(A, torch.int8, dev, "A"), _at(b_t, torch.int32, dev, "b_t"),
-                                    _at(c_t, torch.int8, dev, "c_t"), _at(B, torch.int8, dev, "B"))
+def _triple(r):
+    return (r.b_skip, r.b_branch, r.c) if isinstance(r, Residual) else r
 
 
 def ivit_linear_lora(X, W, bias, b, c, adapters, idx, rows: int, Y, workspace, out_bits: int = 8, skip=None, res=None,
@@ -430,14 +398,8 @@ def ivit_linear_lora(X, W, bias, b, c, adapters, idx, rows: int, Y, workspace, o
     """ivit_linear_requant with a low-rank adapter per request: rows [q * rows, (q + 1) * rows) of X take adapter
     idx[q] of ``adapters`` = (A [n,R,K] int8, b_t [n,R] int32, c_t [n,R] int8, B [n,N,R] int8), or none where idx[q]
     is outside [0, n)."""
-    dev, M, K, N, lora = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y, skip)
-    i8, i32 = torch.int8, torch.int32
-    st = (_lib or lib()).ivit_linear_lora(
-        _at(X, i8, dev, "X"), M, K, _at(W, i8, dev, "W"), N, None if bias is None else _at(bias, i32, dev, "bias"),
-        _at(b, i32, dev, "b"), _at(c, i8, dev, "c"), out_bits, rounding, lora, _at(idx, i32, dev, "idx"), rows,
-        None if skip is None else _at(skip, i8, dev, "skip"), _NO_RESIDUAL if res is None else _res(res),
-        _at(Y, i8, dev, "Y"), _at(workspace, torch.uint8, dev, "workspace"), workspace.numel(),
-        _raw_stream(stream, dev))
+    st = (_calls or _native()).linear_lora(X, W, bias, b, c, adapters, idx, rows, Y, workspace, out_bits, skip,
+                                             _triple(res), stream, rounding)
     if st:
         _check("ivit_linear_lora", st)
     return Y
@@ -446,25 +408,11 @@ def ivit_linear_lora(X, W, bias, b, c, adapters, idx, rows: int, Y, workspace, o
 def ivit_linear_lora_shiftgelu(X, W, bias, b, c, adapters, idx, rows: int, gelu_I0: int, gelu_M: int, gelu_k_out: int,
                                gelu_out, Y, workspace, stream=None, rounding: int = 0):
     """ivit_linear_shiftgelu with an adapter per request, as ivit_linear_lora."""
-    dev, M, K, N, lora = _lora_args(X, W, bias, b, c, adapters, idx, rows, Y)
-    i8, i32 = torch.int8, torch.int32
-    st = (_lib or lib()).ivit_linear_lora_shiftgelu(
-        _at(X, i8, dev, "X"), M, K, _at(W, i8, dev, "W"), N, None if bias is None else _at(bias, i32, dev, "bias"),
-        _at(b, i32, dev, "b"), _at(c, i8, dev, "c"), rounding, lora, _at(idx, i32, dev, "idx"), rows, gelu_I0, gelu_M,
-        gelu_k_out, _dy(gelu_out), _at(Y, i8, dev, "Y"), _at(workspace, torch.uint8, dev, "workspace"),
-        workspace.numel(), _raw_stream(stream, dev))
+    st = (_calls or _native()).linear_lora_shiftgelu(X, W, bias, b, c, adapters, idx, rows, Y, workspace, gelu_I0,
+                                                       gelu_M, gelu_k_out, gelu_out, stream, rounding)
     if st:
         _check("ivit_linear_lora_shiftgelu", st)
     return Y
-
-
-def _norm(n, dev, name):
-    """ivit_norm packed from (gamma, beta, F, M_ln, out), or None."""
-    if n is None:
-        return None
-    gamma, beta, F, M_ln, out = n
-    b, c = (out.b, out.c) if isinstance(out, Dyadic) else out
-    return _pack_norm(_at(gamma, torch.int8, dev, name), _at(beta, torch.int32, dev, name), F, M_ln, b, c)
 
 
 def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, gate=None, gate_rows: int = 1, pre=None,
@@ -472,26 +420,8 @@ def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, g
     """The end of a residual branch in one pass: y = sat_8((b_skip skip + scale_j u) >> c) with u the branch, after
     its I-LayerNorm ``post`` and times its request's row of ``gate``, and z = I-LayerNorm ``pre`` of y.  skip, branch,
     y, z [rows, cols] int8; post and pre (gamma, beta, F, M_ln, out) or None; gate [ceil(rows / gate_rows), cols] int8
-    or None; scale [cols] int32.  Returns (y, z)."""
-    shape = skip.shape
-    rows, cols = shape
-    if branch.shape != shape or y.shape != shape or scale.numel() != cols:
-        raise ValueError("shape mismatch")
-    if (pre is None) != (z is None) or (z is not None and z.shape != shape):
-        raise ValueError("z shape mismatch: z goes with pre")
-    if gate is not None and (gate_rows < 1 or gate.numel() < -(-rows // gate_rows) * cols):
-        raise ValueError(f"gate shape mismatch: one row of {cols} for every {gate_rows} rows")
-    if post is not None and (post[0].numel() != cols or post[1].numel() != cols):
-        raise ValueError("post shape mismatch")
-    if pre is not None and (pre[0].numel() != cols or pre[1].numel() != cols):
-        raise ValueError("pre shape mismatch")
-    dev = _device(skip, "skip")
-    i8 = torch.int8
-    st = (_lib or lib()).ivit_residual_norm(
-        _at(skip, i8, dev, "skip"), _at(branch, i8, dev, "branch"), rows, cols, _norm(post, dev, "post"),
-        None if gate is None else _at(gate, i8, dev, "gate"), gate_rows, _at(scale, torch.int32, dev, "scale"), b_skip, c,
-        _norm(pre, dev, "pre"), _at(y, i8, dev, "y"), None if z is None else _at(z, i8, dev, "z"),
-        _raw_stream(stream, dev))
+    or None; scale [cols] int32.  y and z may each be skip or branch itself.  Returns (y, z)."""
+    st = (_calls or _native()).residual_norm(skip, branch, scale, b_skip, c, y, post, gate, gate_rows, pre, z, stream)
     if st:
         _check("ivit_residual_norm", st)
     return y, z
@@ -501,14 +431,7 @@ def ivit_attention_diff(qkv, B: int, N: int, H: int, logit, k_s: int, I0: int, M
                         stream=None):
     """ctx [B*N, 128*H] from qkv [B*N, 3*128*H]: each head attends with the difference of two Shiftmax maps, the second
     weighted by lam[h] / 2^M (lam [H] int32)."""
-    if qkv.shape != (B * N, 384 * H) or ctx.shape != (B * N, 128 * H):
-        raise ValueError("shape mismatch")
-    if lam.numel() < H:
-        _holds(H, lam=lam)
-    dev = _device(qkv, "qkv")
-    st = (_lib or lib()).ivit_attention_diff(
-        _at(qkv, torch.int8, dev, "qkv"), B, N, H, _dy(logit), k_s, I0, M, k_out, _at(lam, torch.int32, dev, "lam"),
-        _dy(out), _at(ctx, torch.int8, dev, "ctx"), _raw_stream(stream, dev))
+    st = (_calls or _native()).attention_diff(qkv, B, N, H, logit, k_s, I0, M, k_out, lam, out, ctx, stream)
     if st:
         _check("ivit_attention_diff", st)
     return ctx

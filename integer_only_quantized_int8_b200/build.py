@@ -1,4 +1,5 @@
-"""Build the sm_100a shared library ``libivit_b200.so`` in-tree with nvcc.
+"""Build the sm_100a shared library ``libivit_b200.so`` in-tree with nvcc, and
+the native part of the Python binding, ``_binding.so``, with g++.
 
     python -m integer_only_quantized_int8_b200.build [--verbose]
 
@@ -17,12 +18,14 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libivit_b200.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(PKG, "csrc", "binding.cpp")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2",
     "-shared", "-cudart", "static",
-    "--expt-relaxed-constexpr",
+    "--expt-relaxed-constexpr", "--threads", "8",
 ]
 
 
@@ -49,7 +52,32 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def build_binding(force: bool = False) -> str:
+    if not force and os.path.exists(BINDING) and \
+            os.path.getmtime(BINDING) >= max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(ROOT, "include", "ivit.h"))):
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [base, os.path.join(base, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+                os.path.join(cuda, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in includes), "-o", tmp, BINDING_SRC,
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building _binding.so")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
