@@ -249,10 +249,12 @@ IVIT_DEV void sum32(uint32_t (&r)[8], int lim, int32_t base, uint32_t& sum) {
   }
 }
 
-// Pass 3 of one 32-key unit: r becomes P (neg = 127 in every byte: -P) bytes.  dvs e carries
-// P = (Dv e) >> pshift in its top byte; SHR: only after a further shift by rsh.
+// Pass 3 of one 32-key unit: r becomes P or -P bytes.  With X = dvs e, P = (Dv e) >>
+// pshift is X's top byte (SHR: after a further shift by rsh), and -P that of
+// -X + 2^24 - 1, so the sign costs nothing: mul = dvs, add = 0 or mul = -dvs, add =
+// 2^24 - 1 (SHR: |mul| and, byte by byte, -p = (p + 127) ^ 127 for p <= 128).
 template <bool E8, bool SHR, bool RAGGED>
-IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t dvs, int rsh, uint32_t neg) {
+IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t mul, uint32_t add, int rsh, uint32_t neg) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     uint32_t e[4];
@@ -263,14 +265,11 @@ IVIT_DEV void prob32(uint32_t (&r)[8], int lim, int32_t base, uint32_t dvs, int 
       exp4(r[q], base, e);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e[i] *= dvs;
-      if (SHR) e[i] >>= rsh;
-    }
+    for (int i = 0; i < 4; ++i) e[i] = SHR ? (e[i] * mul) >> rsh : e[i] * mul + add;
     uint32_t w = bytes4<true>(e[0], e[1], e[2], e[3]);
+    if (SHR) w = (w + neg) ^ neg;
     if (RAGGED && !E8) w = first_bytes(w, lim - 4 * q);
-    // -p of a byte p <= 128 is (p + 127) ^ 127, without a carry between bytes
-    r[q] = (w + neg) ^ neg;
+    r[q] = w;
   }
 }
 
@@ -493,11 +492,12 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     const int pshift = a.M - (a.k_out - 1);
     const int lsh = max(24 - pshift, 0), rsh = max(pshift - 24, 0);
     const uint32_t neg = g == 1 ? 0x7F7F7F7Fu : 0u;
+    // item = h + H (img + B qt), advanced without divisions
+    int h = (int)blockIdx.x % a.H, img = (int)blockIdx.x / a.H % a.B, qt = (int)blockIdx.x / (a.H * a.B);
+    const int step_h = (int)gridDim.x % a.H, step_i = (int)gridDim.x / a.H;
     uint32_t n = 0;  // chunks seen
     bool ok = true;
     for (int j = 0; j < n_local; ++j) {
-      const int item = (int)blockIdx.x + j * (int)gridDim.x;
-      const int h = item % a.H, qt = item / (a.H * a.B);
       // warps whose rows all lie past the tile or the image's last token skip the passes
       const bool rows = quarter * 32 < min(a.qrows, N - qt * a.qrows);
       uint32_t num = 1u << a.M;  // IntDiv's numerator
@@ -567,20 +567,21 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
         pair_bar(pair);
         sum = (uint32_t)part[2 * kQTile + row] + (uint32_t)part[3 * kQTile + row];
         const uint32_t dvs = (num / max(sum, 1u)) << lsh;
+        const uint32_t mul = g == 0 || rsh != 0 ? dvs : 0u - dvs, add = g == 0 ? 0u : 0x00FFFFFFu;
 
         // ---- pass 3: P in the logits' place
         if (ok) {
           if (rsh == 0)
             stream_units(t_u, u_n, [&](uint32_t(&r)[8], int u) {
               if (E8 || u != u_ragged)
-                prob32<E8, false, false>(r, 32, base, dvs, 0, neg);
+                prob32<E8, false, false>(r, 32, base, mul, add, 0, 0u);
               else
-                prob32<E8, false, true>(r, lim_ragged, base, dvs, 0, neg);
+                prob32<E8, false, true>(r, lim_ragged, base, mul, add, 0, 0u);
               tmem_st8(t_u + (uint32_t)(8 * u), r);
             });
           else
             stream_units(t_u, u_n, [&](uint32_t(&r)[8], int u) {
-              prob32<E8, true, true>(r, u != u_ragged ? 32 : lim_ragged, base, dvs, rsh, neg);
+              prob32<E8, true, true>(r, u != u_ragged ? 32 : lim_ragged, base, mul, 0u, rsh, neg);
               tmem_st8(t_u + (uint32_t)(8 * u), r);
             });
         }
@@ -589,6 +590,16 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[g]);
+      h += step_h;
+      img += step_i;
+      if (h >= a.H) {
+        h -= a.H;
+        ++img;
+      }
+      while (img >= a.B) {
+        img -= a.B;
+        ++qt;
+      }
     }
   } else {
     // ------------------------------------------------------------ readout warps
