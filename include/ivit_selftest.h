@@ -47,9 +47,9 @@ ivit_status ivit_selftest_int_rate(int32_t iters, int32_t *sink, int32_t sink_le
 
 /* Failure path of the production kernels, without a fault.  After this call
  * the next launch of the named kernel -- 1: the INT8 GEMM of every linear
- * layer (ivit_linear_requant, ivit_linear_shiftgelu and the linear layers of
- * ivit_block_forward); 2: the short-sequence attention kernel (ivit_attention
- * with N <= 256) -- has the TMA producer of its first CTA stop before its
+ * layer (ivit_linear_requant, ivit_linear_shiftgelu, their forms with adapters
+ * and the linear layers of ivit_block_forward); 2: the short-sequence attention
+ * kernel (ivit_attention with N <= 256) or the differential one -- has the TMA producer of its first CTA stop before its
  * `index`-th load (a k-slice of the GEMM, an item of the attention), so the
  * tensor-core issuer's bounded wait for that load runs out after one second.
  * The kernel then records IVIT_ERR_TIMEOUT in the device status word, every

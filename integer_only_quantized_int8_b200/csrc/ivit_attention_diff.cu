@@ -93,7 +93,6 @@ inline DiffLayout diff_layout(int N) {
 
 struct DiffArgs {
   int32_t B, N, H;
-  int32_t qrows;  // query rows per tile: 128, 64 or 32
   int32_t logit_b, logit_c, bq;
   int32_t k_s, ks_lo, ks_hi;
   int32_t I0, M, k_out;
@@ -102,6 +101,7 @@ struct DiffArgs {
   DiffLayout L;
   int8_t* ctx;
   int* status;
+  int32_t withhold;  // diagnostic: CTA 0's producer stops before this local item (-1: never)
 };
 
 IVIT_DEV uint32_t pack_sat4_diff(int32_t y0, int32_t y1, int32_t y2, int32_t y3) {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 20);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int qtiles = (N + a.qrows - 1) / a.qrows;
+  const int qtiles = (N + kQTile - 1) / kQTile;
   const int n_items = qtiles * a.H * a.B;
   const int n_local = n_items > (int)blockIdx.x ? (n_items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
   const int D = a.H * kValDim;
@@ -386,13 +386,14 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
         const int h = item % a.H, img = (item / a.H) % a.B, qt = item / (a.H * a.B);
         const int row0 = img * N;
         if (!diff_wait(&qk_empty[s], ph ^ 1, a.status, abort_flag)) break;
+        if (j == a.withhold && blockIdx.x == 0) break;  // diagnostic (ivit_selftest_withhold)
         uint8_t* st = smem + s * L.qk_bytes;
         mbar_arrive_expect_tx(&qk_full[s], (uint32_t)L.qk_bytes);
         for (int m = 0; m < 2; ++m) {
           uint8_t* q = st + m * (kQTile + L.n64) * kHeadDim;
           const int col = h * kValDim + m * kHeadDim;
           for (int i = 0; i < 2; ++i)
-            tma_load_2d(q + i * 64 * kHeadDim, &tm, col, row0 + qt * a.qrows + 64 * i, &qk_full[s]);
+            tma_load_2d(q + i * 64 * kHeadDim, &tm, col, row0 + qt * kQTile + 64 * i, &qk_full[s]);
           for (int i = 0; i < L.n64 / 64; ++i)
             tma_load_2d(q + (kQTile + 64 * i) * kHeadDim, &tm, D + col, row0 + 64 * i, &qk_full[s]);
         }
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     bool ok = true;
     for (int j = 0; j < n_local; ++j) {
       // warps whose rows all lie past the tile or the image's last token skip the passes
-      const bool rows = quarter * 32 < min(a.qrows, N - qt * a.qrows);
+      const bool rows = quarter * 32 < min(kQTile, N - qt * kQTile);
       uint32_t num = 1u << a.M;  // IntDiv's numerator
       if (g == 1) num = (uint32_t)min(max(__ldg(a.lam + h), 0), 1 << a.M);
 
@@ -612,10 +613,10 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       if (ok) ok = diff_wait(o_full, (uint32_t)(j & 1), a.status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      const int nrow = min(a.qrows, N - qt * a.qrows);  // rows of the tile
+      const int nrow = min(kQTile, N - qt * kQTile);  // rows of the tile
       if (ok && quarter * 32 < nrow) {
         const uint32_t t_o = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)L.o_col;
-        int8_t* dst = a.ctx + (int64_t)(img * N + qt * a.qrows + row) * D + h * kValDim;
+        int8_t* dst = a.ctx + (int64_t)(img * N + qt * kQTile + row) * D + h * kValDim;
         if (a.out_fast)
           read_out<true>(t_o, row < nrow, dst, a);
         else
@@ -652,7 +653,6 @@ ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_
   a.B = B;
   a.N = N;
   a.H = H;
-  a.qrows = kQTile;
   const bool fastq = logit.c >= 1 && (int64_t)logit.b < ((int64_t)1 << (logit.c - 1));
   a.logit_b = logit.b;
   a.logit_c = logit.c;
@@ -682,7 +682,8 @@ ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_
   }
   a.ctx = ctx;
   a.status = dc.status;
-  const int64_t items = (int64_t)((N + a.qrows - 1) / a.qrows) * H * B;
+  a.withhold = take_withhold(kWithholdAttention);
+  const int64_t items = (int64_t)((N + kQTile - 1) / kQTile) * H * B;
   if (items > 0x7fffffff) return IVIT_ERR_UNSUPPORTED;
   a.L = diff_layout(N);
   const int smem = a.L.total + 1024;

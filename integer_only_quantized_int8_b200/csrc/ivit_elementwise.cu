@@ -605,9 +605,11 @@ __global__ void __launch_bounds__(kResNormThreads<CPL>, 1) residual_norm_kernel(
   // The next row's chunks are on their way to shared memory while a row is
   // worked on; each thread fetches and reads its own, so nothing is waited for
   // but its own copies.
+  const bool small = a.rows <= INT_MAX;  // a 32-bit division finds the row's gate
+  const uint32_t gate_rows = (uint32_t)(a.gate_rows < INT_MAX ? a.gate_rows : INT_MAX);
   auto fetch = [&](int64_t row) {
     if (row < a.rows) {
-      const int8_t* g = gated ? a.gate + row / a.gate_rows * cols : nullptr;
+      const int8_t* g = gated ? a.gate + (small ? (int64_t)((uint32_t)row / gate_rows) : row / a.gate_rows) * cols : nullptr;
 #pragma unroll
       for (int k = 0; k < CPL; ++k) {
         const int ci = hl + LPR * k;

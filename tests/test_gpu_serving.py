@@ -477,3 +477,44 @@ def test_linear_lora_back_to_back():
         for q in layers:
             t = serving.linear_lora(t, q.W, q.bias, q.b, q.c, q.adapters, q.idx, q.rows)
     np.testing.assert_array_equal(host(bufs[-1]), t)
+
+
+# ---------------------------------------------------------------- bounded waits
+
+def times_out_then_exact(run, want):
+    assert ivit.ivit_stream_status() == 0
+    run(True)
+    assert ivit.ivit_status_string(ivit.ivit_stream_status()) == "IVIT_ERR_TIMEOUT"
+    got = run(False)
+    assert ivit.ivit_stream_status() == 0
+    np.testing.assert_array_equal(got, want)
+
+
+# K = 1024 takes the shared-tile GEMM kernel, K = 384 the own-tile one; 60 one-token requests of 60 adapters the dp4a way
+@pytest.mark.parametrize("K,req,rows,n", [(1024, 5, 197, 4), (384, 5, 197, 4), (1024, 60, 1, 60)])
+def test_linear_lora_producer_stops_and_reports_timeout(K, req, rows, n):
+    q = LoraCase(req, rows, K, 512, 32, n, seed=50)
+    d, y, ws = q.device(), torch.zeros(q.M, 512, dtype=torch.int8, device="cuda"), workspace(q.M, 32)
+
+    def run(stop):
+        if stop:
+            ivit.ivit_selftest_withhold(ivit.SELFTEST_GEMM, 2)
+        ivit.ivit_linear_lora(*d, y, ws)
+        return host(y)
+
+    times_out_then_exact(run, serving.linear_lora(*q.host()))
+
+
+@pytest.mark.parametrize("N", [197, 500])
+def test_attention_diff_producer_stops_and_reports_timeout(N):
+    qkv, lam = diff_inputs(30, N, 3, seed=51)
+    d, dl = dev(qkv), dev(lam)
+    ctx = torch.zeros(30 * N, 384, dtype=torch.int8, device="cuda")
+
+    def run(stop):
+        if stop:
+            ivit.ivit_selftest_withhold(ivit.SELFTEST_ATTENTION, 1)
+        ivit.ivit_attention_diff(d, 30, N, 3, *DIFF_ARGS, dl, (1 << 20, 25), ctx)
+        return host(ctx)
+
+    times_out_then_exact(run, serving.attention_diff(qkv, 30, N, 3, *DIFF_ARGS, lam, (1 << 20, 25)))
