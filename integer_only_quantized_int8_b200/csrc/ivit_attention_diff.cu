@@ -22,8 +22,9 @@
 //           TMEM, four to a column -- a quarter of the score's space, which
 //           frees the score buffer for the next chunk at once and makes 640
 //           keys of two maps fit;
-//   pass 2  looks e = ShiftExp(L - max L) up and sums it;
-//   pass 3  looks e up again and writes P in the logits' place, which is also
+//   pass 2  looks e = ShiftExp(L - max L) up and sums it; where every e fits a byte
+//           (I0 <= 255) it takes the logit's place, summed by dp4a;
+//   pass 3  takes e (or looks it up again) and writes P in the logits' place, which is also
 //           the layout in which the P V MMA takes its A operand from TMEM
 //           (lane = row, four 8-bit values of K per column): P never passes
 //           through shared memory.
@@ -32,6 +33,12 @@
 // lane l reads copy l: no conflicts).  The four warps of a lane quarter's rows
 // (w, w + 4 of each group) split a row's keys; partial maxima and sums meet in
 // shared memory.
+//
+// What bounds it: about 8 integer instructions a score, 10.6 us of the fullest
+// pipe for 64 x 197 tokens in 6 head pairs, against 36.4 us measured (577 tokens,
+// batch 16: 67.8; 197 tokens, 3 pairs, one image: 9.8).  The passes are dependent
+// chains of four warps per scheduler (0.53 instructions a cycle); more warps do
+// not fit the registers and the counters show no pipe above 42 %.
 //
 // Keys past the last one are masked where they lie: out of the maximum and the
 // sum, and to P = 0.  Whatever their logit bytes hold, their table addresses stay
