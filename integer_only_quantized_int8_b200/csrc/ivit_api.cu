@@ -343,16 +343,12 @@ ivit_status check_lora(const ivit_lora* l, const int32_t* idx, int64_t rows, int
   return IVIT_OK;
 }
 
-// A checked linear layer with adapters: the down projection, then the GEMM
-// that takes the up projection along.
+// A checked linear layer with adapters.
 ivit_status enqueue_lora(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
                          const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits, bool round,
                          const ivit_lora* l, const int32_t* idx, int64_t rows, EpiMode mode, const int8_t* skip,
                          ivit_residual res, const GeluParams* gelu, int8_t* Y, void* workspace, cudaStream_t s) {
-  int8_t* T = static_cast<int8_t*>(workspace);
-  const LoraGemm lg{T, l->B, idx, l->n, l->R, rows};
-  const ivit_status st = launch_lora_down(dc, X, M, K, l->A, l->b_t, l->c_t, round, lg, T, s);
-  if (st != IVIT_OK) return st;
+  const LoraGemm lg{static_cast<int8_t*>(workspace), l->A, l->b_t, l->c_t, l->B, idx, l->n, l->R, rows};
   return launch_gemm(dc, X, M, K, W, N, bias, b, c, out_bits, round, mode, skip, res, gelu, Y, s, &lg);
 }
 

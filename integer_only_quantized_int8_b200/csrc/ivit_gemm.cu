@@ -70,6 +70,7 @@
 // kernel has itself waited for all earlier ones before it lets this one start,
 // and writes nothing but t, so X, W and the skip tensor are read and the
 // k-slices multiplied while it runs.
+#include <algorithm>
 #include <climits>
 
 #include "ivit_common.cuh"
@@ -145,6 +146,19 @@ IVIT_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 
+// Piece i of an adapter stage's B rows (this thread's share): rank entries [16 part, + 16) of adapter a.
+IVIT_DEV void fill_b(const LoraArgs<kLoraMma>& lo, int N, int cb, int a, int part, int i, uint32_t sa) {
+  constexpr int kStep = 32 * kFillWarps;
+  const int l = (int)threadIdx.x - kGemmThreads;  // among the filling warps
+  const int8_t* b = lo.B + ((int64_t)a * N + cb * kBM + l) * lo.R + 16 * part;
+#pragma unroll
+  for (int k = 0; k < kBM / kStep; ++k) {
+    const int ch = l + kStep * k;
+    if (cb * kBM + ch < N)
+      cp_async16_zfill(sa + (uint32_t)(ch * kBK + ((i ^ (ch & 7)) << 4)), b + (int64_t)(kStep * k) * lo.R, true);
+  }
+}
+
 // The filling warps: the adapter stages of every tile of this CTA.  Piece u of the axis is
 // rank entries [16 (u % P), + 16) of request q0 + u / P (by adapter: of adapter
 // u / P), P = R / 16; both
@@ -189,15 +203,7 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
         const int r = (u0 + i) / P, part = (u0 + i) - r * P;
         const int32_t a = i >= np ? -1 : (lo.by_adapter ? r : __ldg(lo.idx + (int64_t)q0 + r));
         const bool has = a >= 0 && a < lo.n;
-        if (has) {
-          const int8_t* b = lo.B + ((int64_t)a * N + cb * kBM + l) * lo.R + 16 * part;
-#pragma unroll
-          for (int k = 0; k < kBM / kStep; ++k) {
-            const int ch = l + kStep * k;
-            if (cb * kBM + ch < N)
-              cp_async16_zfill(sa + (uint32_t)(ch * kBK + ((i ^ (ch & 7)) << 4)), b + (int64_t)(kStep * k) * lo.R, true);
-          }
-        }
+        if (has) fill_b(lo, N, cb, a, part, i, sa);
 #pragma unroll
         for (int k = 0; k < (BN + kStep - 1) / kStep; ++k) {
           const int row = l + kStep * k;
@@ -1204,6 +1210,305 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
   }
 }
 
+// ---------------------------------------------------------------------------
+// One-tile variant for small calls with adapters: every CTA has one tile of 128
+// channels x 64 tokens and computes the tile's t itself, so the call is one
+// launch.  Each k-slice is multiplied twice: W X^T onto the tile's accumulator
+// and A X^T onto a second one, A's rows being [request of the tile][rank]
+// (at most 128).  The epilogue warps requantise that one -- rank rows take the
+// place of channels, so the chunk layout of an output slot is also the layout
+// of the t operand -- with zeros outside a row's request, the two filling warps
+// bring B, and the adapter MMAs complete the accumulator.  Every channel tile
+// repeats the work on A, which is idle tensor time here.  (One row through a
+// 768 -> 1008 layer: 6.3 us with a down projection before the GEMM.)
+// ---------------------------------------------------------------------------
+struct FusedLayout {
+  static constexpr int kBN = 64, kStages = 4, kChunks = kBN / 16;
+  static constexpr int kWBytes = kBM * kBK, kXBytes = kBN * kBK;
+  static constexpr int kAOff = kWBytes + kXBytes;       // A's rows within a stage
+  static constexpr int kStageBytes = kAOff + kBM * kBK;  // the MMA reads 128 rows, filled or not
+  static constexpr int kBOff = kStages * kStageBytes;    // adapter slice: B, then t
+  static constexpr int kTOff = kBOff + kBM * kBK;
+  static constexpr int kOutOff = kTOff + kBN * kBK;
+  static constexpr int kPartSlots = (kChunks + kEpiParts - 1) / kEpiParts * kSlotBytes;
+  static constexpr int kBarOff = kOutOff + kEpiParts * kPartSlots;
+  static constexpr int kNumBars = 2 * kStages + 5 + kEpiParts;  // full, empty; ready, dfull, lfull, tfull, drain; skip
+  static constexpr int kSlotOff = kBarOff + kNumBars * 8;
+  static constexpr int kGeluOff = kSlotOff + 16;
+  static constexpr int kAlloc = kGeluOff + 256 + 1024;
+  static constexpr int kTmemCols = 128;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+};
+
+struct FusedArgs {
+  LoraArgs<kLoraMma> lora;
+  const int32_t* b_t;
+  const int8_t* c_t;
+};
+
+template <int EPI, bool NARROW>
+__global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
+    gemm_lora_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                          const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmY,
+                          const __grid_constant__ CUtensorMap tmS, const __grid_constant__ FusedArgs fa,
+                          const GemmArgs args) {
+  using L = FusedLayout;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* ready = empty + L::kStages;  // both accumulators preloaded
+  uint64_t* dfull = ready + 1;           // A X^T done
+  uint64_t* lfull = dfull + 1;           // t and B in shared memory
+  uint64_t* tfull = lfull + 1;           // the tile done
+  uint64_t* drain = tfull + 1;
+  uint64_t* skip_full = drain + 1;       // [kEpiParts]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
+  int8_t* gelu_tab = reinterpret_cast<int8_t*>(smem + L::kGeluOff);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int64_t M = args.M;
+  const int N = args.N;
+  const LoraArgs<kLoraMma>& lo = fa.lora;
+  const int R = lo.R;
+  const int ch_tiles = (N + kBM - 1) / kBM;
+  const int cb = (int)blockIdx.x % ch_tiles, tb = (int)blockIdx.x / ch_tiles;
+  const int64_t tok0 = (int64_t)tb * L::kBN;
+  const int num_kb = (args.K + kBK - 1) / kBK;
+  uint32_t q0;
+  int pieces;
+  lora_span<L::kBN>(lo, M, tb, q0, pieces);
+  const int nreq = pieces / (R / 16);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(ready, kEpiWarps);
+    mbar_init(dfull, 2);
+    mbar_init(lfull, kEpiWarps + kFillWarps);
+    mbar_init(tfull, 2);
+    mbar_init(drain, 2);
+    for (int e = 0; e < kEpiParts; ++e) mbar_init(&skip_full[e], 1);
+    fence_barrier_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmY);
+    if (EPI == kEpiResidual) prefetch_tensormap(&tmS);
+  }
+  if (EPI == kEpiGelu) {
+    for (int i = threadIdx.x; i < 256; i += blockDim.x)
+      gelu_tab[i] = (int8_t)shiftgelu8(i - 128, args.gelu.I0, args.gelu.M, args.gelu.k_out, args.gelu.out.b,
+                                       args.gelu.out.c);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(tslot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tslot;
+  pdl_wait();  // X, idx and the skip tensor come from earlier kernels
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t bytes = (uint32_t)L::kAOff;  // a request without an adapter loads no rows of A
+      for (int r = 0; r < nreq; ++r) {
+        const int32_t a = __ldg(lo.idx + q0 + r);
+        if (a >= 0 && a < lo.n) bytes += (uint32_t)(R * kBK);
+      }
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1, args.status)) break;
+        if (kb == args.withhold && blockIdx.x == 0) break;  // diagnostic (ivit_selftest_withhold)
+        uint8_t* st = smem + stage * L::kStageBytes;
+        mbar_arrive_expect_tx(&full[stage], bytes);
+        tma_load_2d(st, &tmW, kb * kBK, cb * kBM, &full[stage]);
+        tma_load_2d(st + L::kWBytes, &tmX, kb * kBK, (int32_t)tok0, &full[stage]);
+        for (int r = 0; r < nreq; ++r) {
+          const int32_t a = __ldg(lo.idx + q0 + r);
+          if (a >= 0 && a < lo.n) tma_load_3d(st + L::kAOff + r * R * kBK, &tmA, kb * kBK, 0, a, &full[stage]);
+        }
+        if (++stage == L::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ MMA issuers: k-slices in turn
+    if (lane == 0) {
+      const uint32_t idesc = idesc_i8(kBM, L::kBN, true, true, false);
+      const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint32_t d_lo0 = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
+      int stage = warp - 1;
+      uint32_t phase = 0;
+      bool ok = mbar_wait(ready, 0, args.status);
+      tc_fence_after();
+      for (int kb = warp - 1; kb < num_kb && ok; kb += 2) {
+        ok = mbar_wait(&full[stage], phase, args.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t w = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
+        const uint32_t x = w + (uint32_t)(L::kWBytes >> 4), a = w + (uint32_t)(L::kAOff >> 4);
+#pragma unroll
+        for (int k = 0; k < kBK / 32; ++k) {
+          umma_i8_acc(tmem_base + L::kBN, a + 2 * k, d_hi, x + 2 * k, d_hi, idesc);
+          umma_i8_acc(tmem_base, w + 2 * k, d_hi, x + 2 * k, d_hi, idesc);
+        }
+        umma_commit(&empty[stage]);
+        stage += 2;
+        if (stage >= L::kStages) {
+          stage -= L::kStages;
+          phase ^= 1;
+        }
+      }
+      if (ok) {
+        umma_commit(dfull);
+        if (warp == 1) {
+          ok = mbar_wait(lfull, 0, args.status);
+          tc_fence_after();
+          const uint32_t b = d_lo0 + (uint32_t)(L::kBOff >> 4), t = d_lo0 + (uint32_t)(L::kTOff >> 4);
+          for (int k = 0; ok && k < (pieces + 1) / 2; ++k)
+            umma_i8_acc(tmem_base, b + 2 * k, d_hi, t + 2 * k, d_hi, idesc);
+        }
+        if (ok) umma_commit(tfull);
+      }
+      umma_commit(drain);  // all MMAs have finished before TMEM is released
+      mbar_wait(drain, 0, args.status);
+    }
+  } else if (warp >= 3 + kEpiWarps) {
+    // ------------------------------------------------------------ B of the tile's adapters
+    for (int i = 0; i < pieces; ++i) {
+      const int r = i / (R / 16);
+      const int32_t a = __ldg(lo.idx + q0 + r);
+      if (a >= 0 && a < lo.n) fill_b(lo, N, cb, a, i - r * (R / 16), i, smem_u32(smem + L::kBOff));
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(lfull);
+  } else {
+    // ------------------------------------------------------------ t, then the epilogue
+    const int e = warp - 3;
+    const int quarter = warp & 3;
+    const int part = e >> 2;
+    const int c_begin = (L::kChunks * part) / kEpiParts, c_end = (L::kChunks * (part + 1)) / kEpiParts;
+    const uint32_t sel2 = (lane & 2) ? 0x3276u : 0x5410u;
+    const uint32_t sel1 = (lane & 1) ? 0x3715u : 0x6240u;
+    const bool part_lead = (e & 3) == 0 && lane == 0;
+    uint8_t* const slots = smem + L::kOutOff + part * L::kPartSlots;
+    const uint32_t ofs_even = slot_ofs(lane & 3, quarter, lane >> 2, 0), ofs_odd = slot_ofs(lane & 3, quarter, lane >> 2, 1);
+    const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const int ch = cb * kBM + quarter * 32 + lane;
+    const int32_t bias = (args.bias && ch < N) ? __ldg(args.bias + ch) : 0;
+    bias_fill(tlane, c_begin, c_end, bias);
+    bias_fill(tlane + L::kBN, c_begin, c_end, 0);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ready);
+    int n = c_end - c_begin;  // chunks that hold at least one real token
+    while (n > 0 && tok0 + 16 * (c_begin + n - 1) >= M) --n;
+    const bool live = n > 0;
+    if (EPI == kEpiResidual && part_lead && live) {
+      mbar_arrive_expect_tx(&skip_full[part], (uint32_t)(n * kSlotBytes));
+      for (int i = 0; i < n; ++i)
+        tma_load_2d(slots + i * kSlotBytes, &tmS, cb * kBM, (int32_t)(tok0 + 16 * (c_begin + i)), &skip_full[part]);
+    }
+    // this lane's row of the axis: request q0 + rq, its adapter's multiplier, its tokens [t_lo, t_lo + rows) of the tile
+    const int ar = quarter * 32 + lane, rq = ar / R;
+    const int32_t a = rq < nreq ? __ldg(lo.idx + q0 + rq) : -1;
+    const bool has = a >= 0 && a < lo.n;
+    const int64_t at = has ? (int64_t)a * R + (ar - rq * R) : 0;
+    const int32_t tb_ = has ? __ldg(fa.b_t + at) : 0, tc_ = has ? (int32_t)__ldg(fa.c_t + at) : 0;
+    const int64_t t_lo = ((int64_t)q0 + rq) * lo.rows - tok0;
+    const ChanConst kc = ch < N ? chan_const(__ldg(args.b + ch), __ldg(args.c + ch), bias, args.Kacc)
+                                : chan_const(0, 0, 0, args.Kacc);
+    const int req = __all_sync(0xffffffffu, kc.fast)
+                        ? kReqFast
+                        : (__any_sync(0xffffffffu, kc.needs_clamp) ? kReqWideClamp : kReqWide);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(dfull, 0, args.status));
+    tc_fence_after();
+    if (ok) {
+      for (int c = c_begin; c < c_end; ++c) {
+        uint32_t r[16];
+        tmem_ld16(tlane + (uint32_t)(L::kBN + 16 * c), r);
+        tmem_ld_wait_regs(r);
+        uint8_t* slot = smem + L::kTOff + c * kSlotBytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          int32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            int64_t v = (int64_t)tb_ * (int32_t)r[4 * k + i];  // < 2^31 2^28
+            if (args.round && tc_ > 0) v += (int64_t)1 << (tc_ - 1);
+            v >>= tc_;
+            const int64_t tk = 16 * c + 4 * k + i - t_lo;
+            y[i] = has && tk >= 0 && tk < (int64_t)lo.rows ? (int32_t)(v < -128 ? -128 : (v > 127 ? 127 : v)) : 0;
+          }
+          *reinterpret_cast<uint32_t*>(slot + (k >> 1) * 1024 + ((k & 1) ? ofs_odd : ofs_even)) =
+              transpose4x4(pack_sat4(y[0], y[1], y[2], y[3]), sel2, sel1);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (ok && lane == 0) mbar_arrive(lfull);
+    ok = ok && mbar_wait(tfull, 0, args.status);
+    bool got_skip = true;
+    if (EPI == kEpiResidual && live) got_skip = mbar_wait(&skip_full[part], 0, args.status);
+    if (part_bar_and(part, ok && got_skip)) {
+      tc_fence_after();
+#define IVIT_TILE(REQ) \
+  epi_tile<EPI, NARROW, REQ, kLoraNone>(tlane, c_begin, n, kc, args, gelu_tab, slots, ofs_even, ofs_odd, sel2, sel1, \
+                                        LoraArgs<kLoraNone>{}, 0, 0)
+      if (!args.round) {
+        if (req == kReqFast)
+          IVIT_TILE(kReqFast);
+        else if (req == kReqWide)
+          IVIT_TILE(kReqWide);
+        else
+          IVIT_TILE(kReqWideClamp);
+      } else {
+        if (req == kReqFast)
+          IVIT_TILE(kReqFast + kReqRound);
+        else if (req == kReqWide)
+          IVIT_TILE(kReqWide + kReqRound);
+        else
+          IVIT_TILE(kReqWideClamp + kReqRound);
+      }
+#undef IVIT_TILE
+      fence_proxy_async_smem();
+      part_bar_and(part, true);
+      if (part_lead) {
+        for (int i = 0; i < n; ++i)
+          tma_store_2d(&tmY, cb * kBM, (int32_t)(tok0 + 16 * (c_begin + i)), slots + i * kSlotBytes);
+        bulk_commit_group();
+        bulk_wait_all();
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, L::kTmemCols);
+  }
+}
+
 // Entries of a token tile's axis by request (160 tokens stand for every width).
 int64_t lora_requests(const LoraGemm& lg, int64_t M) { return ((M < 160 ? M : 160) - 1) / lg.rows + 2; }
 
@@ -1359,6 +1664,46 @@ LoraKind lora_kind(const LoraGemm& lg, int64_t M, int N, int num_sms) {
   return entries <= (lora_narrow(M, N, num_sms) ? 9 : 56) ? kLoraMma : kLoraEpi;
 }
 
+// Whether every tile of the one-tile variant gets an SM and its requests' ranks fit
+// 128 rows.
+bool lora_one_tile(const LoraGemm& lg, int64_t M, int N, int num_sms) {
+  constexpr int kBN = FusedLayout::kBN;
+  if ((int64_t)((N + kBM - 1) / kBM) * ((M + kBN - 1) / kBN) > num_sms) return false;
+  // most requests that a tile of kBN tokens from a multiple of kBN on can touch
+  const int64_t most = kBN % lg.rows == 0 ? kBN / lg.rows : (kBN - 2) / lg.rows + 2;
+  return std::min(most, M / lg.rows) * lg.R <= kBM;
+}
+
+template <int EPI, bool NARROW>
+ivit_status run_lora_tile(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
+                          const GemmArgs& a, const LoraGemm& lg, cudaStream_t stream) {
+  using L = FusedLayout;
+  CUtensorMap tmW, tmX, tmA, tmY, tmS;
+  const uint64_t K = (uint64_t)a.K, N = (uint64_t)a.N, M = (uint64_t)a.M;
+  ivit_status st = encode_tmap_2d_u8(&tmW, W, K, N, K, kBK, kBM, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == IVIT_OK) st = encode_tmap_2d_u8(&tmX, X, K, M, K, kBK, L::kBN, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == IVIT_OK)
+    st = encode_tmap_3d_u8(&tmA, lg.A, K, (uint64_t)lg.R, (uint64_t)lg.n, kBK, (uint32_t)lg.R, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == IVIT_OK) st = encode_tmap_2d_u8(&tmY, Y, N, M, N, kBM, 16, CU_TENSOR_MAP_SWIZZLE_128B);
+  tmS = tmY;  // unused without a residual
+  if (st == IVIT_OK && EPI == kEpiResidual)
+    st = encode_tmap_2d_u8(&tmS, skip, N, M, N, kBM, 16, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != IVIT_OK) return st;
+  const FusedArgs fa{{nullptr, lg.B, lg.idx, (uint32_t)lg.rows, lg.n, lg.R, 0}, lg.b_t, lg.c_t};
+  auto kern = gemm_lora_tile_kernel<EPI, NARROW>;
+  static bool attr_done[64];  // per device; benign race: the attribute value is the same
+  if (!attr_done[dc.device]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+      return IVIT_ERR_CUDA;
+    attr_done[dc.device] = true;
+  }
+  const int64_t tiles = (int64_t)((a.N + kBM - 1) / kBM) * ((a.M + L::kBN - 1) / L::kBN);
+  const cudaError_t e = launch_pdl(kern, dim3((unsigned)tiles), dim3(gemm_threads<kLoraMma>()), L::kAlloc, stream, tmW, tmX,
+                                   tmA, tmY, tmS, fa, a);
+  note_launch();
+  return e == cudaSuccess ? IVIT_OK : IVIT_ERR_CUDA;
+}
+
 template <int EPI, bool NARROW, int LORA>
 ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                         const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
@@ -1426,6 +1771,22 @@ ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t
   a.status = dc.status;
   a.withhold = take_withhold(kWithholdGemm);
   const bool narrow = out_bits < 8;
+  if (lora && lora_one_tile(*lora, M, N, dc.num_sms)) {
+    switch (mode) {
+      case kEpiPlain:
+        return narrow ? run_lora_tile<kEpiPlain, true>(dc, X, W, skip, Y, a, *lora, stream)
+                      : run_lora_tile<kEpiPlain, false>(dc, X, W, skip, Y, a, *lora, stream);
+      case kEpiResidual:
+        return narrow ? run_lora_tile<kEpiResidual, true>(dc, X, W, skip, Y, a, *lora, stream)
+                      : run_lora_tile<kEpiResidual, false>(dc, X, W, skip, Y, a, *lora, stream);
+      case kEpiGelu:
+        return run_lora_tile<kEpiGelu, false>(dc, X, W, skip, Y, a, *lora, stream);
+    }
+  }
+  if (lora) {
+    const ivit_status st = launch_lora_down(dc, X, M, K, round, *lora, stream);
+    if (st != IVIT_OK) return st;
+  }
   const LoraKind kind = lora ? lora_kind(*lora, M, N, dc.num_sms) : kLoraNone;
 #define IVIT_GEMM_DISPATCH(EPI, NARROW)                                                            \
   (kind == kLoraNone  ? dispatch_bn<EPI, NARROW, kLoraNone>(dc, X, W, skip, Y, a, nullptr, stream) \

@@ -65,21 +65,25 @@ ivit_status encode_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, u
 ivit_status check_block_args(const ivit_block_params* p, const int8_t* x, const int8_t* y, int32_t B, int32_t N);
 
 // Low-rank adapters beside a GEMM: request q = rows [q * rows, (q + 1) * rows)
-// of X adds t B_a^T, a = idx[q], to its accumulators.
+// of X adds t B_a^T, t = sat_8((b_t (X A_a^T)) >> c_t), a = idx[q], to its
+// accumulators.
 struct LoraGemm {
-  const int8_t* T;     // [M x R], written by launch_lora_down
+  int8_t* T;           // [M x R], the workspace
+  const int8_t* A;     // [n x R x K]
+  const int32_t* b_t;  // [n x R]
+  const int8_t* c_t;   // [n x R]
   const int8_t* B;     // [n x N x R]
   const int32_t* idx;  // [M / rows]; outside [0, n): no adapter
   int32_t n, R;
   int64_t rows;
 };
 
-// t = sat_8((b_t (X A_a^T)) >> c_t) [M x R] of every request with an adapter
-// (the rows of the others are left as they were).
-ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* A,
-                             const int32_t* b_t, const int8_t* c_t, bool round, const LoraGemm& lora, int8_t* T,
-                             cudaStream_t stream);
+// t of every request with an adapter into lora.T (the rows of the others are
+// left as they were).
+ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, bool round,
+                             const LoraGemm& lora, cudaStream_t stream);
 
+// With lora, the down projection before the GEMM too (small calls: both in one kernel).
 ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
                         const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits, bool round,
                         EpiMode mode, const int8_t* skip, ivit_residual res, const GeluParams* gelu, int8_t* Y,

@@ -230,9 +230,8 @@ __global__ void __launch_bounds__(kDownThreads)
 
 }  // namespace
 
-ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* A,
-                             const int32_t* b_t, const int8_t* c_t, bool round, const LoraGemm& lora, int8_t* T,
-                             cudaStream_t stream) {
+ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, bool round,
+                             const LoraGemm& lora, cudaStream_t stream) {
   const int64_t requests = M / lora.rows;
   // as many tiles of equal height (a multiple of the swizzle's eight rows) as still go round once
   int64_t per_request = requests < dc.num_sms ? dc.num_sms / requests : 1;
@@ -243,7 +242,7 @@ ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, in
   ivit_status st = encode_tmap_3d_u8(&tmX, X, (uint64_t)K, (uint64_t)lora.rows, (uint64_t)requests, kDownSlice,
                                      (uint32_t)tile_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != IVIT_OK) return st;
-  st = encode_tmap_3d_u8(&tmA, A, (uint64_t)K, (uint64_t)lora.R, (uint64_t)lora.n, kDownSlice, (uint32_t)lora.R,
+  st = encode_tmap_3d_u8(&tmA, lora.A, (uint64_t)K, (uint64_t)lora.R, (uint64_t)lora.n, kDownSlice, (uint32_t)lora.R,
                          CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != IVIT_OK) return st;
   const int num_kb = (K + kDownSlice - 1) / kDownSlice;
@@ -252,7 +251,7 @@ ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, in
   const int need = (num_kb + kIssuers - 1) / kIssuers * kIssuers;
   if (stages > need) stages = need;
   if (stages > kDownMaxStages) stages = kDownMaxStages;
-  const DownArgs a{b_t, c_t, lora.idx, lora.rows, (uint32_t)tiles, tile_rows, K, lora.R, lora.n, round ? 1 : 0, stages, T,
+  const DownArgs a{lora.b_t, lora.c_t, lora.idx, lora.rows, (uint32_t)tiles, tile_rows, K, lora.R, lora.n, round ? 1 : 0, stages, lora.T,
                    dc.status};
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
