@@ -1223,16 +1223,18 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
 // 768 -> 1008 layer: 6.3 us with a down projection before the GEMM.)
 // ---------------------------------------------------------------------------
 struct FusedLayout {
-  static constexpr int kBN = 64, kStages = 4, kChunks = kBN / 16;
+  static constexpr int kBN = 64, kChunks = kBN / 16;
   static constexpr int kWBytes = kBM * kBK, kXBytes = kBN * kBK;
-  static constexpr int kAOff = kWBytes + kXBytes;       // A's rows within a stage
-  static constexpr int kStageBytes = kAOff + kBM * kBK;  // the MMA reads 128 rows, filled or not
-  static constexpr int kBOff = kStages * kStageBytes;    // adapter slice: B, then t
+  // A stage is W, X and as many rows of A as the call's tiles can need (the
+  // MMA reads 128, the rest from whatever follows): the fewer, the deeper the ring.
+  static constexpr int kAOff = kWBytes + kXBytes;
+  static constexpr int kRingBytes = 4 * (kAOff + kBM * kBK), kMaxStages = 8;
+  static constexpr int kBOff = kRingBytes;  // adapter slice: B, then t
   static constexpr int kTOff = kBOff + kBM * kBK;
   static constexpr int kOutOff = kTOff + kBN * kBK;
   static constexpr int kPartSlots = (kChunks + kEpiParts - 1) / kEpiParts * kSlotBytes;
   static constexpr int kBarOff = kOutOff + kEpiParts * kPartSlots;
-  static constexpr int kNumBars = 2 * kStages + 5 + kEpiParts;  // full, empty; ready, dfull, lfull, tfull, drain; skip
+  static constexpr int kNumBars = 2 * kMaxStages + 5 + kEpiParts;  // full, empty; ready, dfull, lfull, tfull, drain; skip
   static constexpr int kSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kGeluOff = kSlotOff + 16;
   static constexpr int kAlloc = kGeluOff + 256 + 1024;
@@ -1244,7 +1246,37 @@ struct FusedArgs {
   LoraArgs<kLoraMma> lora;
   const int32_t* b_t;
   const int8_t* c_t;
+  int32_t stages, stage_bytes;  // an even number
 };
+
+// Issues slices w, w + 2, ... of one of the two products onto the accumulator at d: the
+// rows at `rows` within a stage times X.  With an even ring those are stages of its own.
+IVIT_DEV bool tile_slices(uint32_t d, int rows, uint8_t* smem, const FusedArgs& fa, int num_kb, int w, uint64_t* full,
+                          uint64_t* empty, uint64_t* ready, int* status) {
+  using L = FusedLayout;
+  const uint32_t idesc = idesc_i8(kBM, L::kBN, true, true, false);
+  const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+  const uint32_t lo0 = (uint32_t)d0, hi = (uint32_t)(d0 >> 32);
+  int stage = w;
+  uint32_t phase = 0;
+  if (!mbar_wait(ready, 0, status)) return false;
+  tc_fence_after();
+  for (int kb = w; kb < num_kb; kb += 2) {
+    if (!mbar_wait(&full[stage], phase, status)) return false;
+    tc_fence_after();
+    const uint32_t st = lo0 + (uint32_t)((stage * fa.stage_bytes) >> 4);
+    const uint32_t a = st + (uint32_t)(rows >> 4), x = st + (uint32_t)(L::kWBytes >> 4);
+#pragma unroll
+    for (int k = 0; k < kBK / 32; ++k) umma_i8_acc(d, a + 2 * k, hi, x + 2 * k, hi, idesc);
+    umma_commit(&empty[stage]);
+    stage += 2;
+    if (stage >= fa.stages) {
+      stage -= fa.stages;
+      phase ^= 1;
+    }
+  }
+  return true;
+}
 
 template <int EPI, bool NARROW>
 __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
@@ -1256,8 +1288,8 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  uint64_t* empty = full + L::kStages;
-  uint64_t* ready = empty + L::kStages;  // both accumulators preloaded
+  uint64_t* empty = full + L::kMaxStages;
+  uint64_t* ready = empty + L::kMaxStages;  // both accumulators preloaded
   uint64_t* dfull = ready + 1;           // A X^T done
   uint64_t* lfull = dfull + 1;           // t and B in shared memory
   uint64_t* tfull = lfull + 1;           // the tile done
@@ -1282,15 +1314,15 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
   const int nreq = pieces / (R / 16);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kStages; ++s) {
+    for (int s = 0; s < fa.stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // the issuers of both products
     }
     mbar_init(ready, kEpiWarps);
     mbar_init(dfull, 2);
     mbar_init(lfull, kEpiWarps + kFillWarps);
     mbar_init(tfull, 2);
-    mbar_init(drain, 2);
+    mbar_init(drain, 4);
     for (int e = 0; e < kEpiParts; ++e) mbar_init(&skip_full[e], 1);
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -1319,7 +1351,19 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t bytes = (uint32_t)L::kAOff;  // a request without an adapter loads no rows of A
+      // W and X of the first slices go out before the tile's adapters are known
+      const int early = min(num_kb, fa.stages);
+      auto load_wx = [&](int kb, int stage) {
+        uint8_t* st = smem + stage * fa.stage_bytes;
+        tma_load_2d(st, &tmW, kb * kBK, cb * kBM, &full[stage]);
+        tma_load_2d(st + L::kWBytes, &tmX, kb * kBK, (int32_t)tok0, &full[stage]);
+      };
+      for (int kb = 0; kb < early; ++kb) {
+        if (kb == args.withhold && blockIdx.x == 0) break;  // diagnostic, as below
+        mbar_expect_tx(&full[kb], (uint32_t)L::kAOff);
+        load_wx(kb, kb);
+      }
+      uint32_t bytes = 0;  // of A: a request without an adapter loads none
       for (int r = 0; r < nreq; ++r) {
         const int32_t a = __ldg(lo.idx + q0 + r);
         if (a >= 0 && a < lo.n) bytes += (uint32_t)(R * kBK);
@@ -1329,69 +1373,49 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
       for (int kb = 0; kb < num_kb; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1, args.status)) break;
         if (kb == args.withhold && blockIdx.x == 0) break;  // diagnostic (ivit_selftest_withhold)
-        uint8_t* st = smem + stage * L::kStageBytes;
-        mbar_arrive_expect_tx(&full[stage], bytes);
-        tma_load_2d(st, &tmW, kb * kBK, cb * kBM, &full[stage]);
-        tma_load_2d(st + L::kWBytes, &tmX, kb * kBK, (int32_t)tok0, &full[stage]);
+        mbar_arrive_expect_tx(&full[stage], bytes + (kb < early ? 0u : (uint32_t)L::kAOff));
+        if (kb >= early) load_wx(kb, stage);
         for (int r = 0; r < nreq; ++r) {
           const int32_t a = __ldg(lo.idx + q0 + r);
-          if (a >= 0 && a < lo.n) tma_load_3d(st + L::kAOff + r * R * kBK, &tmA, kb * kBK, 0, a, &full[stage]);
+          if (a >= 0 && a < lo.n)
+            tma_load_3d(smem + stage * fa.stage_bytes + L::kAOff + r * R * kBK, &tmA, kb * kBK, 0, a, &full[stage]);
         }
-        if (++stage == L::kStages) {
+        if (++stage == fa.stages) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
   } else if (warp <= 2) {
-    // ------------------------------------------------------------ MMA issuers: k-slices in turn
+    // ------------------------------------------------------------ W X^T: k-slices in turn
     if (lane == 0) {
-      const uint32_t idesc = idesc_i8(kBM, L::kBN, true, true, false);
-      const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-      const uint32_t d_lo0 = (uint32_t)d0, d_hi = (uint32_t)(d0 >> 32);
-      int stage = warp - 1;
-      uint32_t phase = 0;
-      bool ok = mbar_wait(ready, 0, args.status);
-      tc_fence_after();
-      for (int kb = warp - 1; kb < num_kb && ok; kb += 2) {
-        ok = mbar_wait(&full[stage], phase, args.status);
-        if (!ok) break;
+      bool ok = tile_slices(tmem_base, 0, smem, fa, num_kb, warp - 1, full, empty, ready, args.status);
+      if (ok && warp == 1) {
+        const uint64_t d0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+        const uint32_t b = (uint32_t)d0 + (uint32_t)(L::kBOff >> 4), t = (uint32_t)d0 + (uint32_t)(L::kTOff >> 4);
+        ok = mbar_wait(lfull, 0, args.status);
         tc_fence_after();
-        const uint32_t w = d_lo0 + (uint32_t)(stage * (L::kStageBytes >> 4));
-        const uint32_t x = w + (uint32_t)(L::kWBytes >> 4), a = w + (uint32_t)(L::kAOff >> 4);
-#pragma unroll
-        for (int k = 0; k < kBK / 32; ++k) {
-          umma_i8_acc(tmem_base + L::kBN, a + 2 * k, d_hi, x + 2 * k, d_hi, idesc);
-          umma_i8_acc(tmem_base, w + 2 * k, d_hi, x + 2 * k, d_hi, idesc);
-        }
-        umma_commit(&empty[stage]);
-        stage += 2;
-        if (stage >= L::kStages) {
-          stage -= L::kStages;
-          phase ^= 1;
-        }
+        for (int k = 0; ok && k < (pieces + 1) / 2; ++k)
+          umma_i8_acc(tmem_base, b + 2 * k, (uint32_t)(d0 >> 32), t + 2 * k, (uint32_t)(d0 >> 32),
+                      idesc_i8(kBM, L::kBN, true, true, false));
       }
-      if (ok) {
-        umma_commit(dfull);
-        if (warp == 1) {
-          ok = mbar_wait(lfull, 0, args.status);
-          tc_fence_after();
-          const uint32_t b = d_lo0 + (uint32_t)(L::kBOff >> 4), t = d_lo0 + (uint32_t)(L::kTOff >> 4);
-          for (int k = 0; ok && k < (pieces + 1) / 2; ++k)
-            umma_i8_acc(tmem_base, b + 2 * k, d_hi, t + 2 * k, d_hi, idesc);
-        }
-        if (ok) umma_commit(tfull);
-      }
+      if (ok) umma_commit(tfull);
       umma_commit(drain);  // all MMAs have finished before TMEM is released
       mbar_wait(drain, 0, args.status);
     }
   } else if (warp >= 3 + kEpiWarps) {
-    // ------------------------------------------------------------ B of the tile's adapters
+    // ------------------------------------------------------------ B of the tile's adapters, and A X^T
     for (int i = 0; i < pieces; ++i) {
       const int r = i / (R / 16);
       const int32_t a = __ldg(lo.idx + q0 + r);
       if (a >= 0 && a < lo.n) fill_b(lo, N, cb, a, i - r * (R / 16), i, smem_u32(smem + L::kBOff));
     }
+    if (lane == 0) {
+      if (tile_slices(tmem_base + L::kBN, L::kAOff, smem, fa, num_kb, warp - 3 - kEpiWarps, full, empty, ready, args.status))
+        umma_commit(dfull);
+      umma_commit(drain);
+    }
+    __syncwarp();
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     __syncwarp();
@@ -1439,21 +1463,29 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
     bool ok = __all_sync(0xffffffffu, mbar_wait(dfull, 0, args.status));
     tc_fence_after();
     if (ok) {
-      for (int c = c_begin; c < c_end; ++c) {
+      const ChanConst kt = chan_const(tb_, tc_, 0, args.K);
+      const bool fast = __all_sync(0xffffffffu, kt.fast);
+      for (int c = c_begin; c < c_begin + n; ++c) {  // tokens past the last one are not stored: whatever their t
         uint32_t r[16];
         tmem_ld16(tlane + (uint32_t)(L::kBN + 16 * c), r);
         tmem_ld_wait_regs(r);
         uint8_t* slot = smem + L::kTOff + c * kSlotBytes;
+        const int64_t first = 16 * c - t_lo;  // of the request's tokens
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           int32_t y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            int64_t v = (int64_t)tb_ * (int32_t)r[4 * k + i];  // < 2^31 2^28
-            if (args.round && tc_ > 0) v += (int64_t)1 << (tc_ - 1);
-            v >>= tc_;
-            const int64_t tk = 16 * c + 4 * k + i - t_lo;
-            y[i] = has && tk >= 0 && tk < (int64_t)lo.rows ? (int32_t)(v < -128 ? -128 : (v > 127 ? 127 : v)) : 0;
+            const int32_t acc = (int32_t)r[4 * k + i];
+            if (fast) {
+              y[i] = args.round ? requant_acc<kReqFast + kReqRound>(acc, kt) : requant_acc<kReqFast>(acc, kt);
+            } else {
+              int64_t v = (int64_t)tb_ * acc;  // < 2^31 2^28
+              if (args.round && tc_ > 0) v += (int64_t)1 << (tc_ - 1);
+              v >>= tc_;
+              y[i] = (int32_t)(v < -128 ? -128 : (v > 127 ? 127 : v));
+            }
+            if (!has || (uint64_t)(first + 4 * k + i) >= (uint64_t)lo.rows) y[i] = 0;
           }
           *reinterpret_cast<uint32_t*>(slot + (k >> 1) * 1024 + ((k & 1) ? ofs_odd : ofs_even)) =
               transpose4x4(pack_sat4(y[0], y[1], y[2], y[3]), sel2, sel1);
@@ -1664,14 +1696,19 @@ LoraKind lora_kind(const LoraGemm& lg, int64_t M, int N, int num_sms) {
   return entries <= (lora_narrow(M, N, num_sms) ? 9 : 56) ? kLoraMma : kLoraEpi;
 }
 
+// Most requests that a tile of kBN tokens from a multiple of kBN on can touch.
+int64_t lora_tile_requests(const LoraGemm& lg, int64_t M) {
+  constexpr int kBN = FusedLayout::kBN;
+  const int64_t most = kBN % lg.rows == 0 ? kBN / lg.rows : (kBN - 2) / lg.rows + 2;
+  return std::min(most, M / lg.rows);
+}
+
 // Whether every tile of the one-tile variant gets an SM and its requests' ranks fit
 // 128 rows.
 bool lora_one_tile(const LoraGemm& lg, int64_t M, int N, int num_sms) {
   constexpr int kBN = FusedLayout::kBN;
   if ((int64_t)((N + kBM - 1) / kBM) * ((M + kBN - 1) / kBN) > num_sms) return false;
-  // most requests that a tile of kBN tokens from a multiple of kBN on can touch
-  const int64_t most = kBN % lg.rows == 0 ? kBN / lg.rows : (kBN - 2) / lg.rows + 2;
-  return std::min(most, M / lg.rows) * lg.R <= kBM;
+  return lora_tile_requests(lg, M) * lg.R <= kBM;
 }
 
 template <int EPI, bool NARROW>
@@ -1689,7 +1726,10 @@ ivit_status run_lora_tile(const DeviceCtx& dc, const int8_t* X, const int8_t* W,
   if (st == IVIT_OK && EPI == kEpiResidual)
     st = encode_tmap_2d_u8(&tmS, skip, N, M, N, kBM, 16, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != IVIT_OK) return st;
-  const FusedArgs fa{{nullptr, lg.B, lg.idx, (uint32_t)lg.rows, lg.n, lg.R, 0}, lg.b_t, lg.c_t};
+  const int stage_bytes = L::kAOff + (int)lora_tile_requests(lg, a.M) * lg.R * kBK;
+  const int num_kb = (a.K + kBK - 1) / kBK;
+  const int stages = std::min({(num_kb + 1) / 2 * 2, L::kRingBytes / stage_bytes / 2 * 2, (int)L::kMaxStages});
+  const FusedArgs fa{{nullptr, lg.B, lg.idx, (uint32_t)lg.rows, lg.n, lg.R, 0}, lg.b_t, lg.c_t, stages, stage_bytes};
   auto kern = gemm_lora_tile_kernel<EPI, NARROW>;
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
