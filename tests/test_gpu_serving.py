@@ -441,6 +441,8 @@ def test_adapted_block():
     (500, 3, 640, 576, 112, 3), (90, 7, 1040, 528, 16, 5),
     (3, 333, 528, 2064, 96, 2), (12, 21, 96, 4096, 64, 50),   # an axis by request, several slices long
     (2, 1100, 48, 64, 16, 3),        # a request of several tiles and one that shares its last
+    (20, 197, 768, 2304, 16, 5), (20, 197, 384, 1152, 16, 3), (64, 60, 1040, 1536, 32, 9), (9, 577, 192, 1600, 112, 4),
+    (4, 16, 2064, 256, 32, 3), (1, 3, 4096, 1008, 128, 2), (16, 8, 320, 4096, 16, 20), (5, 130, 16384, 64, 16, 2),  # one kernel
 ])
 @pytest.mark.parametrize("epi", ["plain", "residual", "gelu"])
 def test_linear_lora_ways(req, rows, K, N, R, n, epi):
@@ -490,8 +492,9 @@ def times_out_then_exact(run, want):
     np.testing.assert_array_equal(got, want)
 
 
-# K = 1024 takes the shared-tile GEMM kernel, K = 384 the own-tile one; 60 one-token requests of 60 adapters the dp4a way
-@pytest.mark.parametrize("K,req,rows,n", [(1024, 5, 197, 4), (384, 5, 197, 4), (1024, 60, 1, 60)])
+# K = 1024 takes the shared-tile GEMM kernel, K = 384 the own-tile one, 60 one-token requests of 60 adapters the dp4a way,
+# 5 requests the one-kernel form
+@pytest.mark.parametrize("K,req,rows,n", [(1024, 40, 197, 4), (384, 40, 197, 4), (1024, 60, 1, 60), (1024, 5, 197, 4)])
 def test_linear_lora_producer_stops_and_reports_timeout(K, req, rows, n):
     q = LoraCase(req, rows, K, 512, 32, n, seed=50)
     d, y, ws = q.device(), torch.zeros(q.M, 512, dtype=torch.int8, device="cuda"), workspace(q.M, 32)
