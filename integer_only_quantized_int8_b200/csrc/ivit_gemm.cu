@@ -1703,9 +1703,13 @@ int64_t lora_tile_requests(const LoraGemm& lg, int64_t M) {
   return std::min(most, M / lg.rows);
 }
 
-// Whether every tile of the one-tile variant gets an SM and its requests' ranks fit
-// 128 rows.
-bool lora_one_tile(const LoraGemm& lg, int64_t M, int N, int num_sms) {
+// Whether every tile of the one-tile variant gets an SM, its requests' ranks fit 128
+// rows, and the reduction is short enough for the second product to hide in latency.
+// Measured (us, one kernel / two): 1 row, K = 768, N = 1008, R = 16: 6.2 / 7.0, R = 128:
+// 6.8 / 9.2; 197 rows, K = 768, N = 2304: 7.2 / 7.8; 512 rows, K = 1024, N = 2048, R = 128:
+// 9.0 / 11.8; 1040 rows, K = 2048, N = 1024: 13.4 / 13.5; 1 row, K = 4096: 16.3 / 12.6.
+bool lora_one_tile(const LoraGemm& lg, int64_t M, int K, int N, int num_sms) {
+  if (K > 2048) return false;
   constexpr int kBN = FusedLayout::kBN;
   if ((int64_t)((N + kBM - 1) / kBM) * ((M + kBN - 1) / kBN) > num_sms) return false;
   return lora_tile_requests(lg, M) * lg.R <= kBM;
@@ -1811,7 +1815,7 @@ ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t
   a.status = dc.status;
   a.withhold = take_withhold(kWithholdGemm);
   const bool narrow = out_bits < 8;
-  if (lora && lora_one_tile(*lora, M, N, dc.num_sms)) {
+  if (lora && lora_one_tile(*lora, M, K, N, dc.num_sms)) {
     switch (mode) {
       case kEpiPlain:
         return narrow ? run_lora_tile<kEpiPlain, true>(dc, X, W, skip, Y, a, *lora, stream)
