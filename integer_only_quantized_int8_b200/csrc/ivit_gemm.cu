@@ -1219,7 +1219,8 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
 // place of channels, so the chunk layout of an output slot is also the layout
 // of the t operand -- with zeros outside a row's request, the two filling warps
 // bring B, and the adapter MMAs complete the accumulator.  Every channel tile
-// repeats the work on A, which is idle tensor time here.  (One row through a
+// repeats the work on A, which is idle tensor time here.  A's rows are those of
+// all adapters when they are fewer than the requests a tile can touch.  (One row through a
 // 768 -> 1008 layer: 6.3 us with a down projection before the GEMM.)
 // ---------------------------------------------------------------------------
 struct FusedLayout {
@@ -1248,6 +1249,11 @@ struct FusedArgs {
   const int8_t* c_t;
   int32_t stages, stage_bytes;  // an even number
 };
+
+// The adapter of entry r of a tile's axis (out of range: none).
+IVIT_DEV int32_t axis_adapter(const LoraArgs<kLoraMma>& lo, uint32_t q0, int r) {
+  return lo.by_adapter ? r : __ldg(lo.idx + q0 + r);
+}
 
 // Issues slices w, w + 2, ... of one of the two products onto the accumulator at d: the
 // rows at `rows` within a stage times X.  With an even ring those are stages of its own.
@@ -1365,7 +1371,7 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
       }
       uint32_t bytes = 0;  // of A: a request without an adapter loads none
       for (int r = 0; r < nreq; ++r) {
-        const int32_t a = __ldg(lo.idx + q0 + r);
+        const int32_t a = axis_adapter(lo, q0, r);
         if (a >= 0 && a < lo.n) bytes += (uint32_t)(R * kBK);
       }
       int stage = 0;
@@ -1376,7 +1382,7 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
         mbar_arrive_expect_tx(&full[stage], bytes + (kb < early ? 0u : (uint32_t)L::kAOff));
         if (kb >= early) load_wx(kb, stage);
         for (int r = 0; r < nreq; ++r) {
-          const int32_t a = __ldg(lo.idx + q0 + r);
+          const int32_t a = axis_adapter(lo, q0, r);
           if (a >= 0 && a < lo.n)
             tma_load_3d(smem + stage * fa.stage_bytes + L::kAOff + r * R * kBK, &tmA, kb * kBK, 0, a, &full[stage]);
         }
@@ -1407,7 +1413,7 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
     // ------------------------------------------------------------ B of the tile's adapters, and A X^T
     for (int i = 0; i < pieces; ++i) {
       const int r = i / (R / 16);
-      const int32_t a = __ldg(lo.idx + q0 + r);
+      const int32_t a = axis_adapter(lo, q0, r);
       if (a >= 0 && a < lo.n) fill_b(lo, N, cb, a, i - r * (R / 16), i, smem_u32(smem + L::kBOff));
     }
     if (lane == 0) {
@@ -1448,18 +1454,25 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
       for (int i = 0; i < n; ++i)
         tma_load_2d(slots + i * kSlotBytes, &tmS, cb * kBM, (int32_t)(tok0 + 16 * (c_begin + i)), &skip_full[part]);
     }
-    // this lane's row of the axis: request q0 + rq, its adapter's multiplier, its tokens [t_lo, t_lo + rows) of the tile
+    // this lane's row of the axis: entry rq (request q0 + rq, or adapter rq), its adapter's multiplier
     const int ar = quarter * 32 + lane, rq = ar / R;
-    const int32_t a = rq < nreq ? __ldg(lo.idx + q0 + rq) : -1;
+    const int32_t a = rq < nreq ? axis_adapter(lo, q0, rq) : -1;
     const bool has = a >= 0 && a < lo.n;
     const int64_t at = has ? (int64_t)a * R + (ar - rq * R) : 0;
     const int32_t tb_ = has ? __ldg(fa.b_t + at) : 0, tc_ = has ? (int32_t)__ldg(fa.c_t + at) : 0;
-    const int64_t t_lo = ((int64_t)q0 + rq) * lo.rows - tok0;
     const ChanConst kc = ch < N ? chan_const(__ldg(args.b + ch), __ldg(args.c + ch), bias, args.Kacc)
                                 : chan_const(0, 0, 0, args.Kacc);
     const int req = __all_sync(0xffffffffu, kc.fast)
                         ? kReqFast
                         : (__any_sync(0xffffffffu, kc.needs_clamp) ? kReqWideClamp : kReqWide);
+    // the axis entry of each token of the part's (at most two) chunks, token i's in lane i (and i + 16)
+    static_assert((L::kChunks + kEpiParts - 1) / kEpiParts <= 2, "two chunks a part");
+    auto key_of = [&](int c) -> int {
+      const int64_t tok = tok0 + 16 * c + (lane & 15);
+      const uint32_t tq = (uint32_t)tok / lo.rows;
+      return tok >= M ? -1 : (lo.by_adapter ? __ldg(lo.idx + tq) : (int)(tq - q0));
+    };
+    const int key0 = key_of(c_begin), key1 = key_of(c_begin + 1);
     bool ok = __all_sync(0xffffffffu, mbar_wait(dfull, 0, args.status));
     tc_fence_after();
     if (ok) {
@@ -1470,7 +1483,7 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
         tmem_ld16(tlane + (uint32_t)(L::kBN + 16 * c), r);
         tmem_ld_wait_regs(r);
         uint8_t* slot = smem + L::kTOff + c * kSlotBytes;
-        const int64_t first = 16 * c - t_lo;  // of the request's tokens
+        const int key = c == c_begin ? key0 : key1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           int32_t y[4];
@@ -1485,7 +1498,7 @@ __global__ void __launch_bounds__(gemm_threads<kLoraMma>(), 1)
               v >>= tc_;
               y[i] = (int32_t)(v < -128 ? -128 : (v > 127 ? 127 : v));
             }
-            if (!has || (uint64_t)(first + 4 * k + i) >= (uint64_t)lo.rows) y[i] = 0;
+            if (__shfl_sync(0xffffffffu, key, 4 * k + i) != rq || !has) y[i] = 0;
           }
           *reinterpret_cast<uint32_t*>(slot + (k >> 1) * 1024 + ((k & 1) ? ofs_odd : ofs_even)) =
               transpose4x4(pack_sat4(y[0], y[1], y[2], y[3]), sel2, sel1);
@@ -1703,8 +1716,8 @@ int64_t lora_tile_requests(const LoraGemm& lg, int64_t M) {
   return std::min(most, M / lg.rows);
 }
 
-// Whether every tile of the one-tile variant gets an SM, its requests' ranks fit 128
-// rows, and the reduction is short enough for the second product to hide in latency.
+// Whether every tile of the one-tile variant gets an SM, the ranks of its requests (or of
+// all adapters, if those are fewer) fit 128 rows, and the reduction is short enough for the second product to hide in latency.
 // Measured (us, one kernel / two): 1 row, K = 768, N = 1008, R = 16: 6.2 / 7.0, R = 128:
 // 6.8 / 9.2; 197 rows, K = 768, N = 2304: 7.2 / 7.8; 512 rows, K = 1024, N = 2048, R = 128:
 // 9.0 / 11.8; 1040 rows, K = 2048, N = 1024: 13.4 / 13.5; 1 row, K = 4096: 16.3 / 12.6.
@@ -1712,7 +1725,7 @@ bool lora_one_tile(const LoraGemm& lg, int64_t M, int K, int N, int num_sms) {
   if (K > 2048) return false;
   constexpr int kBN = FusedLayout::kBN;
   if ((int64_t)((N + kBM - 1) / kBM) * ((M + kBN - 1) / kBN) > num_sms) return false;
-  return lora_tile_requests(lg, M) * lg.R <= kBM;
+  return std::min<int64_t>(lora_tile_requests(lg, M), lg.n) * lg.R <= kBM;
 }
 
 template <int EPI, bool NARROW>
@@ -1730,10 +1743,13 @@ ivit_status run_lora_tile(const DeviceCtx& dc, const int8_t* X, const int8_t* W,
   if (st == IVIT_OK && EPI == kEpiResidual)
     st = encode_tmap_2d_u8(&tmS, skip, N, M, N, kBM, 16, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != IVIT_OK) return st;
-  const int stage_bytes = L::kAOff + (int)lora_tile_requests(lg, a.M) * lg.R * kBK;
+  const int64_t requests = lora_tile_requests(lg, a.M);
+  const bool by_adapter = lg.n < requests;
+  const int stage_bytes = L::kAOff + (int)(by_adapter ? lg.n : requests) * lg.R * kBK;
   const int num_kb = (a.K + kBK - 1) / kBK;
   const int stages = std::min({(num_kb + 1) / 2 * 2, L::kRingBytes / stage_bytes / 2 * 2, (int)L::kMaxStages});
-  const FusedArgs fa{{nullptr, lg.B, lg.idx, (uint32_t)lg.rows, lg.n, lg.R, 0}, lg.b_t, lg.c_t, stages, stage_bytes};
+  const FusedArgs fa{{nullptr, lg.B, lg.idx, (uint32_t)lg.rows, lg.n, lg.R, by_adapter ? 1 : 0},
+                    lg.b_t, lg.c_t, stages, stage_bytes};
   auto kern = gemm_lora_tile_kernel<EPI, NARROW>;
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {

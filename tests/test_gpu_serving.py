@@ -442,7 +442,8 @@ def test_adapted_block():
     (3, 333, 528, 2064, 96, 2), (12, 21, 96, 4096, 64, 50),   # an axis by request, several slices long
     (2, 1100, 48, 64, 16, 3),        # a request of several tiles and one that shares its last
     (20, 197, 768, 2304, 16, 5), (20, 197, 384, 1152, 16, 3), (64, 60, 1040, 1536, 32, 9), (9, 577, 192, 1600, 112, 4),
-    (4, 16, 2064, 256, 32, 3), (1, 3, 4096, 1008, 128, 2), (16, 8, 320, 4096, 16, 20), (5, 130, 16384, 64, 16, 2),  # one kernel
+    (4, 16, 2064, 256, 32, 3), (1, 3, 4096, 1008, 128, 2), (16, 8, 320, 4096, 16, 20), (5, 130, 2048, 64, 16, 2),  # one kernel
+    (300, 1, 768, 304, 16, 8), (64, 1, 320, 1008, 32, 4), (77, 3, 144, 528, 128, 1), (45, 7, 208, 640, 48, 2),
 ])
 @pytest.mark.parametrize("epi", ["plain", "residual", "gelu"])
 def test_linear_lora_ways(req, rows, K, N, R, n, epi):
