@@ -242,7 +242,8 @@ typedef struct {
   const int8_t *B;
 } ivit_lora;
 
-/* Bytes of device workspace ivit_linear_lora needs (t of every row).        */
+/* Bytes of device workspace ivit_linear_lora needs (t of every row; small
+ * calls keep t on chip and leave it alone).                                 */
 size_t ivit_linear_lora_workspace_bytes(int64_t M, int32_t R);
 
 /* The linear layer of ivit_linear_requant with an adapter chosen per request:

@@ -1,7 +1,7 @@
 // binding.cpp -- the Python calls of the serving operators, marshalled natively.
 //
 // Their small calls run for 3 to 10 us on the GPU, less than a dozen tensors took
-// to check and pass through ctypes (9.8 to 13.7 us a call; 3 to 6 here).  Same
+// to check and pass through ctypes (9.8 to 13.7 us a call; 3.3 to 6.4 here).  Same
 // checks, same errors as the ctypes wrappers in __init__.py: every tensor must
 // be a contiguous CUDA tensor of its type on the current device and hold what
 // the library reads or writes; a non-OK status comes back as a number for the
