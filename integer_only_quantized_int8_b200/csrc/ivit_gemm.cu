@@ -241,15 +241,32 @@ IVIT_DEV void lora_add(uint32_t (&r)[16], const LoraArgs<kLoraEpi>& lo, int64_t 
   if (mine >= lo.n) mine = -1;
   const int8_t* b0 = lo.B + (int64_t)min(ch, N - 1) * lo.R;
   const int64_t bstep = (int64_t)N * lo.R;
-  for (int p = 0; p < lo.R; p += 16) {
+  // without an adapter (or past the last token): any row, not added
+  auto dot16 = [&](int i, int32_t a, int p) -> int32_t {
+    const int4 tv = *reinterpret_cast<const int4*>(lo.T + min(tok0 + i, M - 1) * lo.R + p);
+    const int4 bv = __ldg(reinterpret_cast<const int4*>(b0 + max(a, 0) * bstep + p));
+    return __dp4a(tv.x, bv.x, __dp4a(tv.y, bv.y, __dp4a(tv.z, bv.z, __dp4a(tv.w, bv.w, 0))));
+  };
+  if (lo.R <= 32) {
+    // sixteen tokens' loads in flight
+    for (int p = 0; p < lo.R; p += 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int32_t a = __shfl_sync(0xffffffffu, mine, i);
+        const int32_t s = dot16(i, a, p);
+        r[i] += a >= 0 ? (uint32_t)s : 0u;
+      }
+    }
+  } else {
+    // longer rows of B: one token's at a time, so that a lane reads its line to the end before it leaves L1
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int32_t a = __shfl_sync(0xffffffffu, mine, i);
-      // without an adapter (or past the last token): any row, not added
-      const int4 tv = *reinterpret_cast<const int4*>(lo.T + min(tok0 + i, M - 1) * lo.R + p);
-      const int4 bv = __ldg(reinterpret_cast<const int4*>(b0 + max(a, 0) * bstep + p));
-      const int32_t s = __dp4a(tv.x, bv.x, __dp4a(tv.y, bv.y, __dp4a(tv.z, bv.z, __dp4a(tv.w, bv.w, 0))));
-      r[i] += a >= 0 ? (uint32_t)s : 0u;
+      if (a < 0) continue;
+      int32_t s = 0;
+#pragma unroll 4
+      for (int p = 0; p < lo.R; p += 16) s += dot16(i, a, p);
+      r[i] += (uint32_t)s;
     }
   }
 }
