@@ -104,7 +104,7 @@ struct GemmArgs {
 };
 
 // The adapters of a launch (see above); empty without.
-enum LoraKind : int { kLoraNone = 0, kLoraMma = 1, kLoraEpi = 2 };
+enum LoraKind : int { kLoraNone = 0, kLoraMma = 1, kLoraEpi = 2, kLoraEpiLong = 3 };  // Long: ranks above 32
 template <int LORA>
 struct LoraArgs {
   const int8_t* T;     // [M x R]
@@ -225,7 +225,8 @@ IVIT_DEV void lora_fill(const LoraArgs<kLoraMma>& lo, int64_t M, int N, int ch_t
 
 // Brings this channel's rows of B for the tokens [tok0, tok0 + n) towards the SM
 // while the accumulator is waited for.
-IVIT_DEV void lora_touch(const LoraArgs<kLoraEpi>& lo, int64_t M, int N, int64_t tok0, int n, int ch) {
+template <int LORA>
+IVIT_DEV void lora_touch(const LoraArgs<LORA>& lo, int64_t M, int N, int64_t tok0, int n, int ch) {
   const int8_t* b0 = lo.B + (int64_t)min(ch, N - 1) * lo.R;
   for (int i = 0; i < n && tok0 + i < M; ++i) {
     const int32_t a = __ldg(lo.idx + (uint32_t)(tok0 + i) / lo.rows);
@@ -233,40 +234,67 @@ IVIT_DEV void lora_touch(const LoraArgs<kLoraEpi>& lo, int64_t M, int N, int64_t
   }
 }
 
+// lora_add for ranks of up to 16 G entries, G = 4 or 8: a lane's own row of B would be
+// a cache line to itself, so G lanes read a channel's row together (32 / G
+// channels per load, consecutive), add their pieces up by shuffles and hand the
+// sum to the channel's lane.  mine: the adapter of token tok0 + (lane & 15), or < 0.
+template <int G>
+IVIT_DEV void lora_add_long(uint32_t (&r)[16], const LoraArgs<kLoraEpiLong>& lo, int64_t M, int N, int64_t tok0, int ch,
+                            int32_t mine) {
+  constexpr int kPer = 32 / G;  // channels per load
+  const int lane = threadIdx.x & 31;
+  const int piece = lane % G, sub = lane / G;
+  const bool in = 16 * piece < lo.R;
+  const int off = in ? 16 * piece : 0;
+  const int ch0 = ch - lane;  // the warp's first channel
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int32_t a = __shfl_sync(0xffffffffu, mine, i);
+    if (a < 0) continue;
+    const int4 tv = in ? *reinterpret_cast<const int4*>(lo.T + (tok0 + i) * lo.R + off) : make_int4(0, 0, 0, 0);
+    const int8_t* b = lo.B + (int64_t)a * N * lo.R + off;
+    int4 bv[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+      bv[j] = __ldg(reinterpret_cast<const int4*>(b + (int64_t)min(ch0 + j * kPer + sub, N - 1) * lo.R));
+    int32_t got = 0;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      int32_t s = __dp4a(tv.x, bv[j].x, __dp4a(tv.y, bv[j].y, __dp4a(tv.z, bv[j].z, __dp4a(tv.w, bv[j].w, 0))));
+#pragma unroll
+      for (int o = 1; o < G; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const int32_t v = __shfl_sync(0xffffffffu, s, (lane % kPer) * G);
+      if (lane / kPer == j) got = v;
+    }
+    r[i] += (uint32_t)got;
+  }
+}
+
 // The epilogue's own adapters: r[i] += t . B_a of token tok0 + i and channel ch.
-IVIT_DEV void lora_add(uint32_t (&r)[16], const LoraArgs<kLoraEpi>& lo, int64_t M, int N, int64_t tok0, int ch) {
+template <int LORA>
+IVIT_DEV void lora_add(uint32_t (&r)[16], const LoraArgs<LORA>& lo, int64_t M, int N, int64_t tok0, int ch) {
   const int lane = threadIdx.x & 31;
   const int64_t tok = tok0 + (lane & 15);
   int32_t mine = tok < M ? __ldg(lo.idx + (uint32_t)tok / lo.rows) : -1;
   if (mine >= lo.n) mine = -1;
-  const int8_t* b0 = lo.B + (int64_t)min(ch, N - 1) * lo.R;
-  const int64_t bstep = (int64_t)N * lo.R;
-  // without an adapter (or past the last token): any row, not added
-  auto dot16 = [&](int i, int32_t a, int p) -> int32_t {
-    const int4 tv = *reinterpret_cast<const int4*>(lo.T + min(tok0 + i, M - 1) * lo.R + p);
-    const int4 bv = __ldg(reinterpret_cast<const int4*>(b0 + max(a, 0) * bstep + p));
-    return __dp4a(tv.x, bv.x, __dp4a(tv.y, bv.y, __dp4a(tv.z, bv.z, __dp4a(tv.w, bv.w, 0))));
-  };
-  if (lo.R <= 32) {
-    // sixteen tokens' loads in flight
+  if constexpr (LORA == kLoraEpiLong) {
+    if (lo.R > 64)
+      lora_add_long<8>(r, lo, M, N, tok0, ch, mine);
+    else
+      lora_add_long<4>(r, lo, M, N, tok0, ch, mine);
+  } else {
+    const int8_t* b0 = lo.B + (int64_t)min(ch, N - 1) * lo.R;
+    const int64_t bstep = (int64_t)N * lo.R;
     for (int p = 0; p < lo.R; p += 16) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 16; ++i) {  // sixteen tokens' loads in flight
         const int32_t a = __shfl_sync(0xffffffffu, mine, i);
-        const int32_t s = dot16(i, a, p);
+        // without an adapter (or past the last token): any row, not added
+        const int4 tv = *reinterpret_cast<const int4*>(lo.T + min(tok0 + i, M - 1) * lo.R + p);
+        const int4 bv = __ldg(reinterpret_cast<const int4*>(b0 + max(a, 0) * bstep + p));
+        const int32_t s = __dp4a(tv.x, bv.x, __dp4a(tv.y, bv.y, __dp4a(tv.z, bv.z, __dp4a(tv.w, bv.w, 0))));
         r[i] += a >= 0 ? (uint32_t)s : 0u;
       }
-    }
-  } else {
-    // longer rows of B: one token's at a time, so that a lane reads its line to the end before it leaves L1
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int32_t a = __shfl_sync(0xffffffffu, mine, i);
-      if (a < 0) continue;
-      int32_t s = 0;
-#pragma unroll 4
-      for (int p = 0; p < lo.R; p += 16) s += dot16(i, a, p);
-      r[i] += (uint32_t)s;
     }
   }
 }
@@ -495,7 +523,7 @@ IVIT_DEV void epi_tile(uint32_t tbase, int c_begin, int n, const ChanConst& kc, 
                        uint32_t sel1, [[maybe_unused]] const LoraArgs<LORA>& lora, [[maybe_unused]] int64_t tok_base,
                        [[maybe_unused]] int ch) {
   const uint32_t t0 = tbase + (uint32_t)(16 * c_begin);
-  if constexpr (LORA == kLoraEpi) {
+  if constexpr (LORA >= kLoraEpi) {
     for (int i = 0; i < n; ++i) {
       uint32_t r[16];
       tmem_ld16(t0 + (uint32_t)(16 * i), r);
@@ -820,7 +848,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
             tma_load_2d(slots + i * kSlotBytes, &tmS, tile_ch, (int32_t)(tok_base + 16 * (c_begin + i)), sbar);
         }
       }
-      if constexpr (LORA == kLoraEpi)
+      if constexpr (LORA >= kLoraEpi)
         if (live) lora_touch(lora, M, N, tok_base + 16 * c_begin, 16 * n, tile_ch + quarter * 32 + lane);
       const bool got = mbar_wait(&tfull[acc], acc_phase, args.status);
       // the whole part has its accumulator and free slots, or gives up together
@@ -836,7 +864,7 @@ __global__ void __launch_bounds__(gemm_threads<LORA>(), 1)
         skip_phase ^= 1;
       }
       tc_fence_after();
-      if (LORA == kLoraEpi && t == (int)blockIdx.x) {
+      if (LORA >= kLoraEpi && t == (int)blockIdx.x) {
         pdl_wait();  // t comes from the kernel before
         pdl_launch_dependents();
       }
@@ -1726,7 +1754,7 @@ bool lora_narrow(int64_t M, int N, int num_sms) { return (int64_t)((N + kBM - 1)
 LoraKind lora_kind(const LoraGemm& lg, int64_t M, int N, int num_sms) {
   const int64_t requests = lora_requests(lg, M);
   const int64_t entries = lg.n < requests ? lg.n : requests;
-  return entries <= (lora_narrow(M, N, num_sms) ? 9 : 56) ? kLoraMma : kLoraEpi;
+  return entries <= (lora_narrow(M, N, num_sms) ? 9 : 56) ? kLoraMma : (lg.R > 32 ? kLoraEpiLong : kLoraEpi);
 }
 
 // Most requests that a tile of kBN tokens from a multiple of kBN on can touch.
@@ -1787,7 +1815,7 @@ ivit_status run_lora_tile(const DeviceCtx& dc, const int8_t* X, const int8_t* W,
 template <int EPI, bool NARROW, int LORA>
 ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                         const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
-  if constexpr (LORA == kLoraEpi) {
+  if constexpr (LORA >= kLoraEpi) {
     // the adapters' part is spread over the SMs as far as the tokens go: the
     // narrowest tiles (one chunk of tokens, one per epilogue part) that still fit in one round
     const int64_t ch_tiles = (a.N + kBM - 1) / kBM;
@@ -1871,7 +1899,8 @@ ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t
 #define IVIT_GEMM_DISPATCH(EPI, NARROW)                                                            \
   (kind == kLoraNone  ? dispatch_bn<EPI, NARROW, kLoraNone>(dc, X, W, skip, Y, a, nullptr, stream) \
    : kind == kLoraMma ? dispatch_bn<EPI, NARROW, kLoraMma>(dc, X, W, skip, Y, a, lora, stream)     \
-                      : dispatch_bn<EPI, NARROW, kLoraEpi>(dc, X, W, skip, Y, a, lora, stream))
+   : kind == kLoraEpi ? dispatch_bn<EPI, NARROW, kLoraEpi>(dc, X, W, skip, Y, a, lora, stream)     \
+                      : dispatch_bn<EPI, NARROW, kLoraEpiLong>(dc, X, W, skip, Y, a, lora, stream))
   switch (mode) {
     case kEpiPlain:
       return narrow ? IVIT_GEMM_DISPATCH(kEpiPlain, true) : IVIT_GEMM_DISPATCH(kEpiPlain, false);
