@@ -286,8 +286,9 @@ typedef struct {
  *   z_ij = I-LayerNorm_pre(y)_ij                                (pre not NULL)
  * skip, branch, y, z [rows x cols] int8 (z unused without pre).  y and z may
  * each be skip or branch itself (in place); any other overlap of an output
- * with another tensor of the call is IVIT_ERR_INVALID_ARG.  gate [ceil(rows / gate_rows) x cols] int8, one row per
- * request of gate_rows rows; scale [cols] int32, any sign: LayerScale's
+ * with another tensor of the call, scale and the norms' gamma and beta among
+ * them, is IVIT_ERR_INVALID_ARG.  gate [ceil(rows / gate_rows) x cols] int8,
+ * one row per request of gate_rows rows; scale [cols] int32, any sign: LayerScale's
  * lambda_j S_n (S_gate) / S_y over the common shift c; b_skip / 2^c ~
  * S_skip / S_y.  Constraints: rows >= 0; cols and both norms' F, M_ln and out
  * as ivit_layernorm; b_skip >= 0; 0 <= c <= 31; gate_rows >= 1.             */

@@ -411,12 +411,17 @@ ivit_status ivit_residual_norm(const int8_t* skip, const int8_t* branch, int64_t
       !aligned16(y) || (gate && !aligned16(gate)) || (pre && !aligned16(z)))
     return IVIT_ERR_INVALID_ARG;
   // a thread writes y and z only where it has read skip and branch before, so an
-  // output in an input's exact place is fine; any other overlap is not
+  // output in an input's exact place is fine; any other overlap is not (the tables
+  // are read by each block when it starts, while others may write already)
   const int64_t n = rows * cols;
   for (const int8_t* out : {y, pre ? z : y}) {
     if ((out != skip && overlap(out, n, skip, n)) || (out != branch && overlap(out, n, branch, n)) ||
-        (gate && overlap(out, n, gate, ((rows - 1) / gate_rows + 1) * cols)))
+        (gate && overlap(out, n, gate, ((rows - 1) / gate_rows + 1) * cols)) ||
+        overlap(out, n, scale, 4 * (int64_t)cols))
       return IVIT_ERR_INVALID_ARG;
+    for (const ivit_norm* t : {post, pre})
+      if (t && (overlap(out, n, t->gamma, cols) || overlap(out, n, t->beta, 4 * (int64_t)cols)))
+        return IVIT_ERR_INVALID_ARG;
   }
   if (pre && overlap(y, n, z, n)) return IVIT_ERR_INVALID_ARG;
   DeviceCtx dc;

@@ -143,3 +143,27 @@ def test_attention_diff_checks():
     assert call(N=641) == 2
     assert call(H=2049) == 2
     assert call(B=0) == 0 and call(N=0) == 0
+
+
+def test_residual_norm_refuses_outputs_over_its_tables():
+    """scale and the norms' gamma and beta are read by every block while others write: no output may lie in them."""
+    L = ivit.lib()
+    X, O, Y, Z, S, PG, PB, NG, NB = (P + i * 0x10000 for i in range(9))
+    cols = 32
+
+    def call(post=True, pre=True, y=Y, z=Z):
+        po, nx = ivit.Norm(PG, PB, 7, 23, D), ivit.Norm(NG, NB, 7, 23, D)
+        return L.ivit_residual_norm(X, O, 4, cols, C.byref(po) if post else None, None, 1, S, 1, 0,
+                                    C.byref(nx) if pre else None, y, z, None)
+
+    out = 4 * cols   # bytes of y and of z
+    for table, size in ((S, 4 * cols), (PG, cols), (PB, 4 * cols), (NG, cols), (NB, 4 * cols)):
+        for at in (table, table + size - 16, table - out + 16):
+            assert call(y=at) == 1, (hex(table), at - table)
+            assert call(z=at) == 1, (hex(table), at - table)
+    assert call(pre=False, y=S, z=None) == 1 and call(pre=False, y=PB, z=None) == 1
+    assert call(post=False, y=NG) == 1 and call(post=False, z=S) == 1
+    if not torch.cuda.is_available():   # beside a table, or where a norm that is not there would lie: past the checks
+        for ok in (dict(y=S + 4 * cols), dict(y=S - out), dict(z=NB + 4 * cols), dict(z=PG - out),
+                   dict(post=False, y=PG), dict(pre=False, y=NB, z=None)):
+            assert call(**ok) in (2, 3), ok
