@@ -272,7 +272,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     shape((a[9] == Py_None) == (a[10] == Py_None) && (a[10] == Py_None || is(tensor(a[10], "z"), rows, cols)), "z");
     if (a[7] != Py_None) {
       shape(gate_rows >= 1, "gate");
-      holds(tensor(a[7], "gate"), (rows + gate_rows - 1) / gate_rows * cols, "gate");
+      holds(tensor(a[7], "gate"), rows == 0 ? 0 : ((rows - 1) / gate_rows + 1) * cols, "gate");
     }
     norm_shape(a[6], cols, "post");
     norm_shape(a[9], cols, "pre");

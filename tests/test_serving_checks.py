@@ -167,3 +167,17 @@ def test_residual_norm_refuses_outputs_over_its_tables():
         for ok in (dict(y=S + 4 * cols), dict(y=S - out), dict(z=NB + 4 * cols), dict(z=PG - out),
                    dict(post=False, y=PG), dict(pre=False, y=NB, z=None)):
             assert call(**ok) in (2, 3), ok
+
+
+@pytest.mark.parametrize("gate_rows", [(1 << 63) - 1, (1 << 63) - 12])
+def test_residual_norm_gate_of_all_rows(gate_rows):
+    """A gate_rows near the largest integer is one gate for every row: the gate still has to hold that row."""
+    r, c = 12, 64
+
+    def call(gate, rows=r):
+        ivit.ivit_residual_norm(i8(rows, c), i8(rows, c), i32(c), 1, 0, i8(rows, c), gate=gate, gate_rows=gate_rows)
+
+    refused(call, i8(0, c))
+    refused(call, i8(c - 1))
+    past_checks(call, i8(1, c))
+    past_checks(call, i8(0, c), rows=0)
