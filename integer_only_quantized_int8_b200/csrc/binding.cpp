@@ -77,23 +77,38 @@ void shape(bool ok, const char* name = "") {
   if (!ok) fail(PyExc_ValueError, *name ? "%s shape mismatch" : "shape mismatch%s", name);
 }
 
-ivit_stream_t stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return (ivit_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  if (PyLong_Check(o)) return (ivit_stream_t)PyLong_AsVoidPtr(o);
-  PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
-  if (!v) throw Error{};
-  const ivit_stream_t s = (ivit_stream_t)PyLong_AsVoidPtr(v);
-  Py_DECREF(v);
-  return s;
+// A stream argument: a handle, an object with a cuda_stream, or None for the
+// current stream of the call's device, which is looked up once that is known.
+struct Stream {
+  bool current;
+  ivit_stream_t handle;
+  ivit_stream_t on(int dev) const {
+    return current ? (ivit_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream() : handle;
+  }
+};
+
+Stream stream_of(PyObject* o) {
+  if (o == Py_None) return Stream{true, nullptr};
+  PyObject* v = PyIndex_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
+  PyObject* n = v ? PyNumber_Index(v) : nullptr;
+  Py_XDECREF(v);
+  if (!n) throw Error{};
+  void* const h = PyLong_AsVoidPtr(n);
+  Py_DECREF(n);
+  if (!h && PyErr_Occurred()) throw Error{};
+  return Stream{false, (ivit_stream_t)h};
 }
 
 // n integers from a sequence
 void numbers(PyObject* o, int32_t* out, Py_ssize_t n) {
   PyObject* f = PySequence_Fast(o, "expected a sequence of integers");
   if (!f) throw Error{};
-  const bool ok = PySequence_Fast_GET_SIZE(f) == n;
+  bool ok = PySequence_Fast_GET_SIZE(f) == n;
   try {
-    for (Py_ssize_t i = 0; ok && i < n; ++i) out[i] = int32(PySequence_Fast_GET_ITEM(f, i));
+    for (Py_ssize_t i = 0; ok && i < n; ++i) {
+      out[i] = int32(PySequence_Fast_GET_ITEM(f, i));
+      ok = PySequence_Fast_GET_SIZE(f) == n;  // a conversion may run any code
+    }
   } catch (Error&) {
     Py_DECREF(f);
     throw;
@@ -110,7 +125,12 @@ ivit_dyadic dyadic(PyObject* o) {
     for (int i = 0; i < 2; ++i) {
       PyObject* a = PyObject_GetAttrString(o, i ? "c" : "b");
       if (!a) throw Error{};
-      v[i] = (int32_t)PyLong_AsLong(a);
+      try {
+        v[i] = int32(a);
+      } catch (Error&) {
+        Py_DECREF(a);
+        throw;
+      }
       Py_DECREF(a);
     }
   }
@@ -218,11 +238,12 @@ Layer layer(PyObject* const* a, PyObject* skip) {
 PyObject* linear_lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 15)) return nullptr;
   return guarded([&]() -> PyObject* {
-    const Layer l = layer(a, a[11]);
     const int32_t out_bits = int32(a[10]), rounding = int32(a[14]);
     int32_t r[3] = {0, 0, 0};
     if (a[12] != Py_None) numbers(a[12], r, 3);
-    const ivit_stream_t s = stream_of(a[13], l.dev);
+    const Stream stream = stream_of(a[13]);
+    const Layer l = layer(a, a[11]);
+    const ivit_stream_t s = stream.on(l.dev);
     return status([&] {
       return g.linear_lora(l.X, l.M, l.K, l.W, l.N, l.bias, l.b, l.c, out_bits, rounding, &l.lora, l.idx, l.rows, l.skip,
                            ivit_residual{r[0], r[1], r[2]}, l.Y, l.ws, l.ws_bytes, s);
@@ -234,10 +255,11 @@ PyObject* linear_lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* linear_lora_shiftgelu(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 16)) return nullptr;
   return guarded([&]() -> PyObject* {
-    const Layer l = layer(a, Py_None);
     const int32_t I0 = int32(a[10]), M = int32(a[11]), k_out = int32(a[12]), rounding = int32(a[15]);
     const ivit_dyadic out = dyadic(a[13]);
-    const ivit_stream_t s = stream_of(a[14], l.dev);
+    const Stream stream = stream_of(a[14]);
+    const Layer l = layer(a, Py_None);
+    const ivit_stream_t s = stream.on(l.dev);
     return status([&] {
       return g.linear_lora_shiftgelu(l.X, l.M, l.K, l.W, l.N, l.bias, l.b, l.c, rounding, &l.lora, l.idx, l.rows, I0, M,
                                      k_out, out, l.Y, l.ws, l.ws_bytes, s);
@@ -245,18 +267,19 @@ PyObject* linear_lora_shiftgelu(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// gamma, beta, F, M_ln, out; shapes first, so that every size is checked before any pointer is taken
-void norm_shape(PyObject* o, int64_t cols, const char* name) {
-  if (o == Py_None) return;
+// gamma, beta, F, M_ln, out; shapes and numbers first, so that all of them are checked before any pointer is taken
+ivit_norm norm_shape(PyObject* o, int64_t cols, const char* name) {
+  if (o == Py_None) return ivit_norm{};
   if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5)
     fail(PyExc_TypeError, "%s must be a tuple (gamma, beta, F, M_ln, out)", name);
   shape(tensor(PyTuple_GET_ITEM(o, 0), name).numel() == cols && tensor(PyTuple_GET_ITEM(o, 1), name).numel() == cols, name);
+  return ivit_norm{nullptr, nullptr, int32(PyTuple_GET_ITEM(o, 2)), int32(PyTuple_GET_ITEM(o, 3)),
+                   dyadic(PyTuple_GET_ITEM(o, 4))};
 }
 const ivit_norm* norm(PyObject* o, int dev, const char* name, ivit_norm* n) {
   if (o == Py_None) return nullptr;
-  *n = ivit_norm{i8(THPVariable_Unpack(PyTuple_GET_ITEM(o, 0)), dev, name),
-                 i32(THPVariable_Unpack(PyTuple_GET_ITEM(o, 1)), dev, name), int32(PyTuple_GET_ITEM(o, 2)),
-                 int32(PyTuple_GET_ITEM(o, 3)), dyadic(PyTuple_GET_ITEM(o, 4))};
+  n->gamma = i8(THPVariable_Unpack(PyTuple_GET_ITEM(o, 0)), dev, name);
+  n->beta = i32(THPVariable_Unpack(PyTuple_GET_ITEM(o, 1)), dev, name);
   return n;
 }
 
@@ -274,16 +297,16 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       shape(gate_rows >= 1, "gate");
       holds(tensor(a[7], "gate"), rows == 0 ? 0 : ((rows - 1) / gate_rows + 1) * cols, "gate");
     }
-    norm_shape(a[6], cols, "post");
-    norm_shape(a[9], cols, "pre");
+    ivit_norm np = norm_shape(a[6], cols, "post"), nn = norm_shape(a[9], cols, "pre");
+    const int32_t b_skip = int32(a[3]), c = int32(a[4]);
+    const Stream stream = stream_of(a[11]);
     const int dev = device(skip, "skip");
-    ivit_norm np, nn;
     const ivit_norm *post = norm(a[6], dev, "post", &np), *pre = norm(a[9], dev, "pre", &nn);
     const int8_t *ps = i8(skip, dev, "skip"), *pb = i8(branch, dev, "branch");
     const int8_t* pg = a[7] == Py_None ? nullptr : i8(THPVariable_Unpack(a[7]), dev, "gate");
-    const int32_t *sc = i32(scale, dev, "scale"), b_skip = int32(a[3]), c = int32(a[4]);
+    const int32_t* sc = i32(scale, dev, "scale");
     int8_t *py = i8(y, dev, "y"), *pz = a[10] == Py_None ? nullptr : i8(THPVariable_Unpack(a[10]), dev, "z");
-    const ivit_stream_t s = stream_of(a[11], dev);
+    const ivit_stream_t s = stream.on(dev);
     return status([&] {
       return g.residual_norm(ps, pb, rows, (int32_t)cols, post, pg, gate_rows, sc, b_skip, c, pre, py, pz, s);
     });
@@ -298,13 +321,14 @@ PyObject* attention_diff(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t B = int32(a[1]), N = int32(a[2]), H = int32(a[3]);
     shape(is(qkv, (int64_t)B * N, 384 * (int64_t)H) && is(ctx, (int64_t)B * N, 128 * (int64_t)H));
     holds(lam, H, "lam");
-    const int dev = device(qkv, "qkv");
     const ivit_dyadic logit = dyadic(a[4]), out = dyadic(a[10]);
     const int32_t k_s = int32(a[5]), I0 = int32(a[6]), M = int32(a[7]), k_out = int32(a[8]);
+    const Stream stream = stream_of(a[12]);
+    const int dev = device(qkv, "qkv");
     const int8_t* q = i8(qkv, dev, "qkv");
     const int32_t* l = i32(lam, dev, "lam");
     int8_t* o = i8(ctx, dev, "ctx");
-    const ivit_stream_t s = stream_of(a[12], dev);
+    const ivit_stream_t s = stream.on(dev);
     return status([&] { return g.attention_diff(q, B, N, H, logit, k_s, I0, M, k_out, l, out, o, s); });
   });
 }

@@ -181,3 +181,85 @@ def test_residual_norm_gate_of_all_rows(gate_rows):
     refused(call, i8(c - 1))
     past_checks(call, i8(1, c))
     past_checks(call, i8(0, c), rows=0)
+
+
+class Fields:
+    def __init__(self, b, c):
+        self.b, self.c = b, c
+
+
+class Raw:
+    def __init__(self, cuda_stream):
+        self.cuda_stream = cuda_stream
+
+
+def test_bad_plain_arguments_raise():
+    """Numbers, dyadics and streams that do not convert raise before anything is passed on; none is cut to 32 bits."""
+    r, c = 12, 64
+
+    def diff(B=2, N=9, H=2, logit=(1, 0), k_s=8, I0=4, M=30, k_out=8, out=(1, 0), stream=None):
+        ivit.ivit_attention_diff(i8(18, 768), B, N, H, logit, k_s, I0, M, k_out, i32(2), out, i8(18, 256), stream=stream)
+
+    def norm(b_skip=1, shift=0, n=None, stream=None):
+        ivit.ivit_residual_norm(i8(r, c), i8(r, c), i32(c), b_skip, shift, i8(r, c), post=n, stream=stream)
+
+    def tables(F=7, M=23, out=(1, 0)):
+        return dict(n=(i8(c), i32(c), F, M, out))
+
+    def lora(bits=8, res=(1, 1, 1), stream=None, rounding=0):
+        ad = (i8(3, 16, 64), i32(3, 16), i8(3, 16), i8(3, 48, 16))
+        ivit.ivit_linear_lora(i8(32, 64), i8(48, 64), None, i32(48), i8(48), ad, i32(4), 8, i8(32, 48),
+                              torch.zeros(512, dtype=torch.uint8), bits, i8(32, 48), res, stream, rounding)
+
+    def gelu(I0=4, M=30, k_out=8, out=(1, 0), stream=None, rounding=0):
+        ad = (i8(3, 16, 64), i32(3, 16), i8(3, 16), i8(3, 48, 16))
+        ivit.ivit_linear_lora_shiftgelu(i8(32, 64), i8(48, 64), None, i32(48), i8(48), ad, i32(4), 8, I0, M, k_out, out,
+                                        i8(32, 48), torch.zeros(512, dtype=torch.uint8), stream, rounding)
+
+    def raises(error, fn, **k):
+        with pytest.raises(error):
+            fn(**k)
+
+    for fn in (diff, norm, lora, gelu):
+        past_checks(fn)
+        for ok in (0, Raw(0), Raw(1 << 40)):
+            past_checks(fn, stream=ok)
+        raises(AttributeError, fn, stream=object())
+        raises(TypeError, fn, stream=Raw("0"))
+        raises(OverflowError, fn, stream=1 << 70)
+        raises(OverflowError, fn, stream=Raw(1 << 70))
+    for bad, error in ((Fields("1", 0), TypeError), (Fields(1, None), TypeError), (Fields(1.5, 0), TypeError),
+                       (Fields(1 << 32, 0), OverflowError), (Fields(1, 1 << 80), OverflowError), (object(), AttributeError),
+                       ((1, "0"), TypeError), ((1 << 32, 0), OverflowError), ((1,), ValueError), ((1, 0, 0), ValueError)):
+        raises(error, diff, logit=bad)
+        raises(error, diff, out=bad)
+        raises(error, gelu, out=bad)
+        raises(error, norm, **tables(out=bad))
+    past_checks(diff, logit=ivit.Dyadic(1, 0), out=Fields(1, 0))
+    past_checks(norm, **tables(out=ivit.Dyadic(1, 0)))
+    for v, error in ((None, TypeError), (1.5, TypeError), (1 << 31, OverflowError), (1 << 64, OverflowError)):
+        for k in ("B", "N", "H", "k_s", "I0", "M", "k_out"):
+            raises(error, diff, **{k: v})
+        for k in ("b_skip", "shift"):
+            raises(error, norm, **{k: v})
+        raises(error, norm, **tables(F=v))
+        raises(error, norm, **tables(M=v))
+        for k in ("bits", "rounding"):
+            raises(error, lora, **{k: v})
+        raises(error, lora, res=(1, v, 1))
+        for k in ("I0", "M", "k_out", "rounding"):
+            raises(error, gelu, **{k: v})
+
+
+def test_a_sequence_that_shrinks_while_it_is_read():
+    """A list emptied by the conversion of its first element is not read past its end."""
+    pair = []
+
+    class Empties:
+        def __index__(self):
+            pair.clear()
+            return 1
+
+    pair += [Empties(), 0]
+    with pytest.raises(ValueError):
+        ivit.ivit_attention_diff(i8(18, 768), 2, 9, 2, pair, 8, 4, 30, 8, i32(2), (1, 0), i8(18, 256))
