@@ -12,6 +12,7 @@ built, importing works but the first call raises (build it with
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 import threading
 
@@ -235,12 +236,14 @@ def _native():
     """The native marshalling of the serving operators' calls (csrc/binding.cpp), bound to the loaded library."""
     global _calls
     if _calls is None:
-        L = lib()
-        try:
-            from . import _binding as m
-        except ImportError as e:
-            raise RuntimeError("the native binding is missing: build it with "
-                               "`python -m integer_only_quantized_int8_b200.build`") from e
+        from .build import binding_path
+        L, path = lib(), binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError("the native binding is missing for this Python and torch: build it with "
+                               "`python -m integer_only_quantized_int8_b200.build`")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
         m.bind(*(C.cast(f, C.c_void_p).value for f in (L.ivit_linear_lora, L.ivit_linear_lora_shiftgelu,
                                                        L.ivit_residual_norm, L.ivit_attention_diff)))
         _calls = m
