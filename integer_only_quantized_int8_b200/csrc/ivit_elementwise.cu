@@ -548,11 +548,11 @@ __device__ __forceinline__ void row_sum2(int32_t& s1, int32_t& s2) {
 // gamma (sign-extended), beta or the scale as 16-byte groups of four
 // channels, [q][chunk] as in layernorm_staged_kernel
 __device__ __forceinline__ void stage_gamma(int4* dst, const int8_t* g, int i, int nchunk) {
-  const uint32_t g4 = __ldg(reinterpret_cast<const uint32_t*>(g) + i);
+  const uint32_t g4 = __ldcg(reinterpret_cast<const uint32_t*>(g) + i);
   dst[(i & 3) * nchunk + (i >> 2)] = make_int4(sext_byte(g4, 0), sext_byte(g4, 1), sext_byte(g4, 2), sext_byte(g4, 3));
 }
 __device__ __forceinline__ void stage_i32(int4* dst, const int32_t* t, int i, int nchunk) {
-  dst[(i & 3) * nchunk + (i >> 2)] = __ldg(reinterpret_cast<const int4*>(t) + i);
+  dst[(i & 3) * nchunk + (i >> 2)] = __ldcg(reinterpret_cast<const int4*>(t) + i);
 }
 
 // The requants' forms and the gate are decided per launch, not per element (a
@@ -567,6 +567,10 @@ enum ResNormForm : int { kFormAny = 0, kFormFast = 1, kFormFastGate = 2 };
 // 80 per thread at three 16-byte chunks a lane, 128 at four.
 template <int CPL>
 constexpr int kResNormThreads = CPL <= 3 ? 768 : 512;
+
+// Towards the L2, which is where a kernel that still runs writes to: allowed before
+// the dependent-launch wait, as what is read after it is current all the same.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -583,22 +587,37 @@ __global__ void __launch_bounds__(kResNormThreads<CPL>, 1) residual_norm_kernel(
   int4* const s_nb = s_ng + (PRE ? 4 * nchunk : 0);
   // a thread's own chunks of the next row it takes: [branch, skip, gate][chunk][thread]
   int4* const s_next = s_nb + (PRE ? 4 * nchunk : 0) + threadIdx.x;
-  for (int i = threadIdx.x; i < cols / 4; i += blockDim.x) {
-    stage_i32(s_scale, a.scale, i, nchunk);
-    if (POST) {
-      stage_gamma(s_pg, a.post.gamma, i, nchunk);
-      stage_i32(s_pb, a.post.beta, i, nchunk);
-    }
-    if (PRE) {
-      stage_gamma(s_ng, a.pre.gamma, i, nchunk);
-      stage_i32(s_nb, a.pre.beta, i, nchunk);
-    }
-  }
-  __syncthreads();
-  pdl_wait();  // skip, branch and gate come from earlier kernels
-  pdl_launch_dependents();
   const int hl = threadIdx.x % LPR;
   const int groups = blockDim.x / LPR;  // rows in hand at once
+  // row = (group of lanes) * blocks + block: the rows of a block lie apart, but
+  // every block has as many as any other
+  const int64_t step = (int64_t)groups * gridDim.x;
+  int64_t row = (int64_t)(threadIdx.x / LPR) * gridDim.x + blockIdx.x;
+  // The tables may come from the kernel just before (a conditioning layer's output,
+  // say), as skip and branch do: they are brought towards the L2 before the wait, and
+  // read after it.  (Reading the tables after it alone took 12608 x 768 from 17.0 to 18.0 us;
+  // the first rows' prefetch wins that back.)
+  for (int i = threadIdx.x; i < cols / 32; i += blockDim.x) {
+    prefetch_l2(a.scale + 32 * i);
+    if (POST) {
+      prefetch_l2(a.post.beta + 32 * i);
+      if (i % 4 == 0) prefetch_l2(a.post.gamma + 32 * i);
+    }
+    if (PRE) {
+      prefetch_l2(a.pre.beta + 32 * i);
+      if (i % 4 == 0) prefetch_l2(a.pre.gamma + 32 * i);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < CPL; ++k) {
+    const int ci = hl + LPR * k;
+    if (row < a.rows && ci < nchunk && hl % 2 == 0) {  // one lane per 32-byte sector
+      prefetch_l2(a.branch + row * cols + 16 * ci);
+      prefetch_l2(a.skip + row * cols + 16 * ci);
+    }
+  }
+  pdl_wait();  // skip, branch and gate come from earlier kernels
+  pdl_launch_dependents();
   constexpr bool kFast = FORM != kFormAny;
   const bool gated = FORM == kFormFastGate || (FORM == kFormAny && a.gate);
   int32_t plo = INT_MIN, phi = INT_MAX, nlo = INT_MIN, nhi = INT_MAX;
@@ -624,11 +643,19 @@ __global__ void __launch_bounds__(kResNormThreads<CPL>, 1) residual_norm_kernel(
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // row = (group of lanes) * blocks + block: the rows of a block lie apart, but
-  // every block has as many as any other
-  const int64_t step = (int64_t)groups * gridDim.x;
-  int64_t row = (int64_t)(threadIdx.x / LPR) * gridDim.x + blockIdx.x;
   fetch(row);
+  for (int i = threadIdx.x; i < cols / 4; i += blockDim.x) {  // behind the first rows' copies
+    stage_i32(s_scale, a.scale, i, nchunk);
+    if (POST) {
+      stage_gamma(s_pg, a.post.gamma, i, nchunk);
+      stage_i32(s_pb, a.post.beta, i, nchunk);
+    }
+    if (PRE) {
+      stage_gamma(s_ng, a.pre.gamma, i, nchunk);
+      stage_i32(s_nb, a.pre.beta, i, nchunk);
+    }
+  }
+  __syncthreads();
   for (int64_t row0 = blockIdx.x; row0 < a.rows; row0 += step, row += step) {  // the same trips for a warp's lanes
     const bool active = row < a.rows;
     const int64_t base = (active ? row : 0) * cols;

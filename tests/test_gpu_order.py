@@ -1,0 +1,115 @@
+"""Tables that the call just before writes, on the same stream: a kernel that starts
+while its predecessor finishes must not read them early.  The predecessor is a call
+of this library (an exact copy of a large tensor that holds the tables), since
+its kernels let the next one start before they end."""
+import numpy as np
+import pytest
+import torch
+
+import integer_only_quantized_int8_b200 as ivit
+import oracle
+import synthetic
+from integer_only_quantized_int8_b200 import build as ivit_build
+from integer_only_quantized_int8_b200 import params as ivit_params
+from oracle import serving
+
+pytestmark = pytest.mark.gpu
+
+CALLS = 40
+OUT = (400000000, 30)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ivit_build.build()
+    yield
+    assert ivit.ivit_stream_status() == 0
+
+
+class Tables:
+    """Two sets of tables, each somewhere in a large tensor of its own, and a tensor that takes the one or the other."""
+    ROWS, COLS = 4096, 768
+
+    def __init__(self, sets, place):
+        self.at, n = {}, 0
+        for name, t in sets[0].items():
+            self.at[name] = (n, t.dtype, t.size)
+            n += -(-t.nbytes // 256) * 256
+        first = {"first": 0, "last": (self.ROWS * self.COLS - n) // 256 * 256}[place]
+        self.src = []
+        for s in sets:
+            h = np.random.default_rng(1).integers(-128, 128, self.ROWS * self.COLS, dtype=np.int8)
+            for name, t in s.items():
+                o = first + self.at[name][0]
+                h[o:o + t.nbytes] = t.view(np.int8)
+            self.src.append(torch.from_numpy(h.reshape(self.ROWS, self.COLS)).cuda())
+        self.dst = torch.zeros(self.ROWS, self.COLS, dtype=torch.int8, device="cuda")
+        self.zero = torch.zeros(self.COLS, dtype=torch.int32, device="cuda")
+        self.first = first
+
+    def view(self, name):
+        o, dtype, size = self.at[name]
+        o += self.first
+        t = self.dst.view(-1)[o:o + size * dtype.itemsize]
+        return t if dtype == np.int8 else t.view(torch.int32)
+
+    def write(self, i):
+        """dst = src[i], by a call of the library."""
+        ivit.ivit_residual_norm(self.src[i], self.src[i], self.zero, 1, 0, self.dst)
+
+
+def norm_tables(r, cols, name):
+    return {name + "_gamma": r.integers(-128, 128, cols, dtype=np.int8),
+            name + "_beta": r.integers(-3000, 3000, cols, dtype=np.int32)}
+
+
+def run(tables, call, outputs, graph):
+    """CALLS calls, the tables changed before each one; outputs[k]: what call k writes."""
+    def all_calls():
+        for k in range(CALLS):
+            tables.write(k & 1)
+            call(k)
+
+    if graph:
+        tables.write(0)
+        call(0)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            all_calls()
+        for o in outputs:
+            for t in o:
+                t.zero_()
+        g.replay()
+    else:
+        torch.cuda.synchronize()
+        all_calls()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 192), (394, 768), (3000, 1024)])
+@pytest.mark.parametrize("place", ["first", "last"])
+@pytest.mark.parametrize("graph", [False, True])
+def test_branch_end_tables_of_the_call_before(rows, cols, place, graph):
+    r = np.random.default_rng(rows + cols)
+    sets = [{"scale": r.integers(-(1 << 28), 1 << 28, cols).astype(np.int32), **norm_tables(r, cols, "post"),
+             **norm_tables(r, cols, "pre")} for _ in range(2)]
+    t = Tables(sets, place)
+    x, o = (r.integers(-128, 128, (rows, cols), dtype=np.int8) for _ in range(2))
+    dx, do = torch.from_numpy(x).cuda(), torch.from_numpy(o).cuda()
+    outs = [(torch.zeros_like(dx), torch.zeros_like(dx)) for _ in range(CALLS)]
+
+    def norm(n):
+        return t.view(n + "_gamma"), t.view(n + "_beta"), 7, 23, OUT
+
+    def call(k):
+        ivit.ivit_residual_norm(dx, do, t.view("scale"), 1 << 29, 30, outs[k][0], post=norm("post"), pre=norm("pre"),
+                                z=outs[k][1])
+
+    run(t, call, outs, graph)
+    want = [serving.residual_norm(x, o, s["scale"], 1 << 29, 30, (s["post_gamma"], s["post_beta"], 7, 23, OUT),
+                                  pre=(s["pre_gamma"], s["pre_beta"], 7, 23, OUT)) for s in sets]
+    assert (want[0][0] != want[1][0]).any() and (want[0][1] != want[1][1]).any()
+    for k in range(CALLS):
+        for got, w in zip(outs[k], want[k & 1]):
+            np.testing.assert_array_equal(got.cpu().numpy(), w)
