@@ -275,7 +275,7 @@ ivit_status ivit_layernorm(const int8_t* x, int64_t rows, int32_t cols, const in
   DeviceCtx dc;
   ivit_status st = device_ctx(&dc);
   if (st != IVIT_OK) return st;
-  return launch_layernorm(dc, x, rows, cols, gamma, beta, F, M_ln, out, y, (cudaStream_t)stream);
+  return launch_layernorm(dc, x, rows, cols, gamma, beta, F, M_ln, out, false, y, (cudaStream_t)stream);
 }
 
 ivit_status ivit_shiftgelu_rowmax(const int8_t* x, int64_t rows, int32_t cols, int32_t I0, int32_t M,
@@ -505,9 +505,10 @@ ivit_status check_block(const ivit_block_params* p, const int8_t* x, const int8_
   return IVIT_OK;
 }
 
-// Enqueues one checked block (B, N > 0).
+// Enqueues one checked block (B, N > 0).  first: nothing of the same library call
+// precedes it on the stream.
 ivit_status enqueue_block(const DeviceCtx& dc, const ivit_block_params* p, const int8_t* x, int8_t* y,
-                          void* workspace, int32_t B, int32_t N, cudaStream_t s) {
+                          void* workspace, int32_t B, int32_t N, bool first, cudaStream_t s) {
   const int32_t D = p->D, Dm = p->Dm;
   const int64_t T = (int64_t)B * N;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -520,7 +521,8 @@ ivit_status enqueue_block(const DeviceCtx& dc, const ivit_block_params* p, const
   const ivit_residual none{0, 0, 0};
   ivit_status st;
   // a1 LN1
-  if ((st = launch_layernorm(dc, x, T, D, p->ln1_gamma, p->ln1_beta, p->ln_F, p->ln_M, p->ln1_out, ln, s)) != IVIT_OK)
+  if ((st = launch_layernorm(dc, x, T, D, p->ln1_gamma, p->ln1_beta, p->ln_F, p->ln_M, p->ln1_out, !first, ln, s)) !=
+      IVIT_OK)
     return st;
   // a2 QKV
   const bool rnd = p->linear_round != 0;
@@ -536,7 +538,7 @@ ivit_status enqueue_block(const DeviceCtx& dc, const ivit_block_params* p, const
                         xh, s)) != IVIT_OK)
     return st;
   // a7 LN2
-  if ((st = launch_layernorm(dc, xh, T, D, p->ln2_gamma, p->ln2_beta, p->ln_F, p->ln_M, p->ln2_out, ln, s)) !=
+  if ((st = launch_layernorm(dc, xh, T, D, p->ln2_gamma, p->ln2_beta, p->ln_F, p->ln_M, p->ln2_out, true, ln, s)) !=
       IVIT_OK)
     return st;
   // a8 + a9 fc1 with ShiftGELU in the epilogue
@@ -557,7 +559,7 @@ ivit_status ivit_block_forward(const ivit_block_params* p, const int8_t* x, int8
   if (st != IVIT_OK || B == 0 || N == 0) return st;
   DeviceCtx dc;
   if ((st = device_ctx(&dc)) != IVIT_OK) return st;
-  return enqueue_block(dc, p, x, y, workspace, B, N, (cudaStream_t)stream);
+  return enqueue_block(dc, p, x, y, workspace, B, N, true, (cudaStream_t)stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -644,7 +646,7 @@ ivit_status enqueue_head(const DeviceCtx& dc, const int8_t* x, int32_t B, int32_
   int8_t* n = t + up((size_t)B * D);
   ivit_status st;
   if ((st = launch_gather_rows(dc, x, B, Ntok, D, t, s)) != IVIT_OK) return st;
-  if ((st = launch_layernorm(dc, t, B, D, gamma, beta, F, M_ln, ln_out, n, s)) != IVIT_OK) return st;
+  if ((st = launch_layernorm(dc, t, B, D, gamma, beta, F, M_ln, ln_out, true, n, s)) != IVIT_OK) return st;
   return launch_gemm(dc, n, B, D, W, Ncls, bias, b, c, 8, round, kEpiPlain, nullptr, ivit_residual{0, 0, 0}, nullptr,
                      logits,
                      s);
@@ -730,7 +732,7 @@ ivit_status ivit_model_forward(const ivit_model_params* m, const int8_t* img, in
                                 m->linear_round != 0, m->cls, m->pos, m->pos_add, scratch, tok[0], s)) != IVIT_OK)
     return st;
   for (int32_t i = 0; i < m->n_blocks; ++i)
-    if ((st = enqueue_block(dc, &m->blocks[i], tok[i & 1], tok[(i + 1) & 1], scratch, B, Ntok, s)) != IVIT_OK)
+    if ((st = enqueue_block(dc, &m->blocks[i], tok[i & 1], tok[(i + 1) & 1], scratch, B, Ntok, false, s)) != IVIT_OK)
       return st;
   return enqueue_head(dc, tok[m->n_blocks & 1], B, Ntok, m->D, m->head_gamma, m->head_beta, m->head_ln_F,
                       m->head_ln_M, m->head_ln_out, m->w_head, m->Ncls, m->bias_head, m->b_head, m->c_head,

@@ -139,8 +139,10 @@ ivit_status launch_attention_diff(const DeviceCtx& dc, const int8_t* qkv, int32_
                                   ivit_dyadic logit, int32_t k_s, int32_t I0, int32_t M, int32_t k_out,
                                   const int32_t* lam, ivit_dyadic out, int8_t* ctx, cudaStream_t stream);
 
+// tables_ready: gamma and beta were written before a kernel that the same library
+// call enqueued earlier on the stream.
 ivit_status launch_layernorm(const DeviceCtx& dc, const int8_t* x, int64_t rows, int32_t cols,
                              const int8_t* gamma, const int32_t* beta, int32_t F, int32_t M_ln, ivit_dyadic out,
-                             int8_t* y, cudaStream_t stream);
+                             bool tables_ready, int8_t* y, cudaStream_t stream);
 
 }  // namespace ivit

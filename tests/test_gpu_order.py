@@ -113,3 +113,45 @@ def test_branch_end_tables_of_the_call_before(rows, cols, place, graph):
     for k in range(CALLS):
         for got, w in zip(outs[k], want[k & 1]):
             np.testing.assert_array_equal(got.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 192), (394, 768), (3000, 1024)])
+@pytest.mark.parametrize("place", ["first", "last"])
+@pytest.mark.parametrize("graph", [False, True])
+def test_layernorm_tables_of_the_call_before(rows, cols, place, graph):
+    r = np.random.default_rng(rows + cols)
+    sets = [norm_tables(r, cols, "ln") for _ in range(2)]
+    t = Tables(sets, place)
+    x = r.integers(-128, 128, (rows, cols), dtype=np.int8)
+    dx = torch.from_numpy(x).cuda()
+    outs = [(torch.zeros_like(dx),) for _ in range(CALLS)]
+    run(t, lambda k: ivit.ivit_layernorm(dx, t.view("ln_gamma"), t.view("ln_beta"), 7, 23, OUT, outs[k][0]), outs, graph)
+    want = [oracle.layernorm(x, s["ln_gamma"], s["ln_beta"], 7, 23, OUT) for s in sets]
+    assert (want[0] != want[1]).any()
+    for k in range(CALLS):
+        np.testing.assert_array_equal(outs[k][0].cpu().numpy(), want[k & 1])
+
+
+@pytest.mark.parametrize("place", ["first", "last"])
+def test_block_tables_of_the_call_before(place):
+    """Both norms' tables of an encoder block; the block's later kernels take them for granted."""
+    B, N, D = 2, 65, 192
+    wl = synthetic.make_workload(B=B, N=N, D=D, H=3, Dm=768, seed=21, n_cal=2)
+    p = ivit_params.integer_params(wl.blocks[0])
+    names = ("ln1_gamma", "ln1_beta", "ln2_gamma", "ln2_beta")
+    dtypes = (np.int8, np.int32) * 2
+    one = {n: np.ascontiguousarray(p[n]).astype(d) for n, d in zip(names, dtypes)}
+    two = {n: np.ascontiguousarray(t[::-1]) for n, t in one.items()}
+    t = Tables([one, two], place)
+    dp = ivit_params.to_device(p, torch.device("cuda"))
+    for n in names:
+        setattr(dp.c, n, t.view(n).data_ptr())
+    x = torch.from_numpy(wl.x).cuda()
+    outs = [(torch.zeros_like(x),) for _ in range(CALLS)]
+    ws = torch.empty(ivit.ivit_block_workspace_bytes(B, N, D, 768), dtype=torch.uint8, device="cuda")
+    run(t, lambda k: ivit.ivit_block_forward(dp, x, outs[k][0], ws, B, N), outs, False)
+    q = oracle.block_params(wl.blocks[0])
+    want = [oracle.block_forward({**q, **s}, wl.x, B, N) for s in (one, two)]
+    assert (want[0] != want[1]).any()
+    for k in range(CALLS):
+        np.testing.assert_array_equal(outs[k][0].cpu().numpy(), want[k & 1])
