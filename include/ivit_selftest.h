@@ -61,6 +61,21 @@ ivit_status ivit_selftest_int_rate(int32_t iters, int32_t *sink, int32_t sink_le
  * IVIT_ERR_INVALID_ARG for another kernel number or a negative index.      */
 ivit_status ivit_selftest_withhold(int32_t kernel, int32_t index);
 
+/* Which kernel ivit_linear_lora (gelu != 0: ivit_linear_lora_shiftgelu) takes
+ * on a GPU of `sms` SMs for M tokens in requests of `rows`, K -> N channels and
+ * n adapters of rank R.  Host only; nothing is enqueued and no device needed.
+ *   form[0]  1: one kernel for the layer and its adapters; else a down
+ *            projection, whose result joins the layer's accumulators 2: as
+ *            further k-slices, 3: by dp4a (ranks up to 32), 4: by dp4a (above)
+ *   form[1]  tokens of a tile
+ *   form[2]  forms 1 and 2: 1 when the adapters' reduction axis runs over all
+ *            adapters, 0 over the requests of a tile
+ *   form[3]  1: the GEMM whose epilogue parts drain tiles of their own
+ * Returns IVIT_ERR_INVALID_ARG for sizes that the layer refuses, sms < 1 or a
+ * NULL form.                                                                */
+ivit_status ivit_selftest_lora_form(int64_t M, int32_t K, int32_t N, int32_t n, int32_t R, int64_t rows,
+                                    int32_t gelu, int32_t sms, int32_t *form);
+
 #ifdef __cplusplus
 }
 #endif

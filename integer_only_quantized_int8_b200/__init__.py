@@ -28,7 +28,7 @@ __all__ = [
     "ivit_model_workspace_bytes", "ivit_model_forward", "ivit_selftest_wait_timeout", "ivit_selftest_int_rate",
     "ivit_shiftgelu_rowmax", "ivit_attention_lis", "ivit_layernorm_ptf", "ivit_selftest_withhold",
     "Lora", "Norm", "ivit_linear_lora_workspace_bytes", "ivit_linear_lora", "ivit_linear_lora_shiftgelu",
-    "ivit_residual_norm", "ivit_attention_diff",
+    "ivit_residual_norm", "ivit_attention_diff", "ivit_selftest_lora_form",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -47,7 +47,7 @@ EXPORTED_SYMBOLS = (
     "ivit_selftest_wait_timeout", "ivit_selftest_int_rate",
     "ivit_shiftgelu_rowmax", "ivit_attention_lis", "ivit_layernorm_ptf", "ivit_selftest_withhold",
     "ivit_linear_lora_workspace_bytes", "ivit_linear_lora", "ivit_linear_lora_shiftgelu", "ivit_residual_norm",
-    "ivit_attention_diff",
+    "ivit_attention_diff", "ivit_selftest_lora_form",
 )
 
 _STATUS = {0: "IVIT_OK", 1: "IVIT_ERR_INVALID_ARG", 2: "IVIT_ERR_UNSUPPORTED", 3: "IVIT_ERR_CUDA",
@@ -188,6 +188,8 @@ def lib() -> C.CDLL:
             L.ivit_attention_diff.argtypes = [vp, i32, i32, i32, Dyadic, i32, i32, i32, i32, vp, Dyadic, vp, vp]
             L.ivit_selftest_withhold.restype = C.c_int
             L.ivit_selftest_withhold.argtypes = [i32, i32]
+            L.ivit_selftest_lora_form.restype = C.c_int
+            L.ivit_selftest_lora_form.argtypes = [i64, i32, i32, i32, i32, i64, i32, i32, C.POINTER(i32)]
             L.ivit_selftest_int_rate.restype = C.c_int
             L.ivit_selftest_int_rate.argtypes = [i32, vp, i32, C.POINTER(C.c_int64), vp]
             _lib = L
@@ -492,6 +494,15 @@ def ivit_selftest_wait_timeout(stream=None):
 
 SELFTEST_GEMM = 1
 SELFTEST_ATTENTION = 2
+
+
+def ivit_selftest_lora_form(M: int, K: int, N: int, n: int, R: int, rows: int, gelu: bool = False, sms: int = 148):
+    """The kernel that a layer with adapters takes on a GPU of ``sms`` SMs: (way, tokens of a tile, by adapter, own
+    tiles); see include/ivit_selftest.h.  Needs no GPU."""
+    form = (C.c_int32 * 4)()
+    _check("ivit_selftest_lora_form", lib().ivit_selftest_lora_form(int(M), int(K), int(N), int(n), int(R), int(rows),
+                                                                    int(bool(gelu)), int(sms), form))
+    return tuple(form)
 
 
 def ivit_selftest_withhold(kernel: int, index: int):

@@ -1741,8 +1741,18 @@ bool use_own_tiles(int K) {
   return K <= 512 || (EPI == kEpiGelu && K <= 768);
 }
 
+// Tokens of a kLoraEpi tile: the adapters' part is spread over the SMs as far as the
+// tokens go, by the narrowest tiles (one chunk of tokens, one per epilogue part)
+// that still fit in one round.
+int lora_epi_bn(int64_t M, int N, int num_sms) {
+  const int64_t ch_tiles = (N + kBM - 1) / kBM;
+  return ch_tiles * ((M + 15) / 16) <= num_sms ? 16 : (ch_tiles * ((M + 47) / 48) <= num_sms ? 48 : 128);
+}
+
 // Whether kLoraEpi's narrow tiles go round the SMs once.
-bool lora_narrow(int64_t M, int N, int num_sms) { return (int64_t)((N + kBM - 1) / kBM) * ((M + 47) / 48) <= num_sms; }
+bool lora_narrow(int64_t M, int N, int num_sms) { return lora_epi_bn(M, N, num_sms) <= 48; }
+
+constexpr int kLoraWidest = 192;  // tokens of a shared-tile GEMM's tile beside adapters, at most
 
 // How a launch's adapters join the accumulators.  The MMA way costs with the
 // length of the axis, min(requests of a tile, adapters) entries, the dp4a way
@@ -1816,14 +1826,14 @@ template <int EPI, bool NARROW, int LORA>
 ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, const int8_t* skip, int8_t* Y,
                         const GemmArgs& a, const LoraGemm* lg, cudaStream_t stream) {
   if constexpr (LORA >= kLoraEpi) {
-    // the adapters' part is spread over the SMs as far as the tokens go: the
-    // narrowest tiles (one chunk of tokens, one per epilogue part) that still fit in one round
-    const int64_t ch_tiles = (a.N + kBM - 1) / kBM;
-    if (ch_tiles * ((a.M + 15) / 16) <= dc.num_sms)
-      return run_gemm<16, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    if (lora_narrow(a.M, a.N, dc.num_sms))
-      return run_gemm<48, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
-    return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+    switch (lora_epi_bn(a.M, a.N, dc.num_sms)) {
+      case 16:
+        return run_gemm<16, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      case 48:
+        return run_gemm<48, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+      default:
+        return run_gemm<128, 6, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
+    }
   } else {
     // beside adapters at most 192 tokens a tile: a ring of four (two MMA issuers) and
     // the adapters' stage fit there (ViT-B QKV 25.5 us; 27.7 with 224 and a ring of three)
@@ -1838,7 +1848,7 @@ ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, c
           return run_gemm_own<128, 4, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
       }
     }
-    switch (pick_bn(a.M, a.N, dc.num_sms, kPlain ? 256 : 192)) {
+    switch (pick_bn(a.M, a.N, dc.num_sms, kPlain ? 256 : kLoraWidest)) {
       case 256:
         if constexpr (kPlain) return run_gemm<256, 3, EPI, NARROW, LORA>(dc, X, W, skip, Y, a, lg, stream);
         [[fallthrough]];
@@ -1858,6 +1868,17 @@ ivit_status dispatch_bn(const DeviceCtx& dc, const int8_t* X, const int8_t* W, c
 }
 
 }  // namespace
+
+LoraForm lora_form(const LoraGemm& lg, int64_t M, int32_t K, int32_t N, bool gelu, int num_sms) {
+  if (lora_one_tile(lg, M, K, N, num_sms))
+    return LoraForm{LoraForm::kOneKernel, FusedLayout::kBN, lg.n < lora_tile_requests(lg, M), false};
+  const LoraKind kind = lora_kind(lg, M, N, num_sms);
+  if (kind != kLoraMma)
+    return LoraForm{kind == kLoraEpi ? LoraForm::kDp4a : LoraForm::kDp4aLong, lora_epi_bn(M, N, num_sms), false, false};
+  const bool own = gelu ? use_own_tiles<kEpiGelu>(K) : use_own_tiles<kEpiPlain>(K);
+  return LoraForm{LoraForm::kMma, own ? pick_bn_own(M, N, num_sms) : pick_bn(M, N, num_sms, kLoraWidest),
+                  lg.n < lora_requests(lg, M), own};
+}
 
 ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
                         const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits, bool round,

@@ -83,6 +83,16 @@ struct LoraGemm {
 ivit_status launch_lora_down(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, bool round,
                              const LoraGemm& lora, cudaStream_t stream);
 
+// The kernel that launch_gemm takes for a layer with adapters (only the sizes in lg are looked at).
+struct LoraForm {
+  enum Way : int { kOneKernel = 1, kMma = 2, kDp4a = 3, kDp4aLong = 4 };  // dp4a: ranks to 32, above
+  Way way;
+  int tokens;       // of a tile
+  bool by_adapter;  // the reduction axis runs over the adapters, not the tile's requests
+  bool own_tiles;   // the own-tile GEMM
+};
+LoraForm lora_form(const LoraGemm& lg, int64_t M, int32_t K, int32_t N, bool gelu, int num_sms);
+
 // With lora, the down projection before the GEMM too (small calls: both in one kernel).
 ivit_status launch_gemm(const DeviceCtx& dc, const int8_t* X, int64_t M, int32_t K, const int8_t* W, int32_t N,
                         const int32_t* bias, const int32_t* b, const int8_t* c, int32_t out_bits, bool round,

@@ -110,3 +110,20 @@ extern "C" ivit_status ivit_selftest_withhold(int32_t kernel, int32_t index) {
   ivit::g_withhold.store(((uint64_t)(uint32_t)kernel << 32) | (uint32_t)index, std::memory_order_release);
   return IVIT_OK;
 }
+
+extern "C" ivit_status ivit_selftest_lora_form(int64_t M, int32_t K, int32_t N, int32_t n, int32_t R, int64_t rows,
+                                               int32_t gelu, int32_t sms, int32_t* form) {
+  if (!form || sms < 1 || M < 1 || M > 0x7fffff00LL || K < 16 || K % 16 != 0 || K > 16384 || N < 16 || N % 16 != 0 ||
+      n < 1 || R < 16 || R > 128 || R % 16 != 0 || rows < 1 || M % rows != 0)
+    return IVIT_ERR_INVALID_ARG;
+  ivit::LoraGemm lg{};
+  lg.n = n;
+  lg.R = R;
+  lg.rows = rows;
+  const ivit::LoraForm f = ivit::lora_form(lg, M, K, N, gelu != 0, sms);
+  form[0] = f.way;
+  form[1] = f.tokens;
+  form[2] = f.by_adapter ? 1 : 0;
+  form[3] = f.own_tiles ? 1 : 0;
+  return IVIT_OK;
+}
