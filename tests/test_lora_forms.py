@@ -122,3 +122,22 @@ def test_lora_form_parity(shape, form, several, epi):
         np.testing.assert_array_equal(host(y), want)
         assert untouched()
     assert ivit.ivit_stream_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("req,K,N,R,n", [(60, 768, 784, 16, 60), (512, 272, 2048, 128, 64), (512, 1024, 1024, 32, 64),
+                                         (12, 272, 400, 16, 3), (3000, 784, 784, 48, 2)])
+def test_calls_in_a_row_on_one_workspace(req, K, N, R, n):
+    """The same rows of t are written and read by call after call, each with other rows and adapters: none may see what
+    the one before left there."""
+    q = [LoraCase(req, 1, K, N, R, n, seed=60 + i) for i in range(3)]
+    for t in q[1:]:
+        t.W, t.bias, t.b, t.c, t.adapters = q[0].W, q[0].bias, q[0].b, q[0].c, q[0].adapters
+    d, ws = [t.device() for t in q], workspace(req, R)
+    ys = [dev(np.zeros((req, N), np.int8)) for _ in range(60)]
+    for i, y in enumerate(ys):
+        ivit.ivit_linear_lora(*d[i % 3], y, ws)
+    want = [serving.linear_lora(*t.host()) for t in q]
+    for i, y in enumerate(ys):
+        np.testing.assert_array_equal(host(y), want[i % 3])
+    assert ivit.ivit_stream_status() == 0
