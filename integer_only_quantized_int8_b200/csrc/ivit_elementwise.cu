@@ -558,15 +558,38 @@ __device__ __forceinline__ void row_sum2(int32_t& s1, int32_t& s2) {
   }
 }
 
-// gamma (sign-extended), beta or the scale as 16-byte groups of four
-// channels, [q][chunk] as in layernorm_staged_kernel
-__device__ __forceinline__ void stage_gamma(int4* dst, const int8_t* g, int i, int nchunk) {
-  const uint32_t g4 = __ldcg(reinterpret_cast<const uint32_t*>(g) + i);
-  dst[(i & 3) * nchunk + (i >> 2)] = make_int4(sext_byte(g4, 0), sext_byte(g4, 1), sext_byte(g4, 2), sext_byte(g4, 3));
-}
-__device__ __forceinline__ void stage_i32(int4* dst, const int32_t* t, int i, int nchunk) {
-  dst[(i & 3) * nchunk + (i >> 2)] = __ldcg(reinterpret_cast<const int4*>(t) + i);
-}
+// Four channels of the per-channel tables, as a thread brings them to shared memory
+// (gamma sign-extended), where they lie [q][chunk] as in layernorm_staged_kernel.
+template <bool POST, bool PRE>
+struct ResNormTables {
+  int4 scale, post_beta, pre_beta;
+  uint32_t post_gamma, pre_gamma;
+  __device__ __forceinline__ void load(const ResNormArgs& a, int i) {
+    scale = __ldcg(reinterpret_cast<const int4*>(a.scale) + i);
+    if (POST) {
+      post_beta = __ldcg(reinterpret_cast<const int4*>(a.post.beta) + i);
+      post_gamma = __ldcg(reinterpret_cast<const uint32_t*>(a.post.gamma) + i);
+    }
+    if (PRE) {
+      pre_beta = __ldcg(reinterpret_cast<const int4*>(a.pre.beta) + i);
+      pre_gamma = __ldcg(reinterpret_cast<const uint32_t*>(a.pre.gamma) + i);
+    }
+  }
+  static __device__ __forceinline__ int4 widen(uint32_t g) {
+    return make_int4(sext_byte(g, 0), sext_byte(g, 1), sext_byte(g, 2), sext_byte(g, 3));
+  }
+  __device__ __forceinline__ void store(int4* s_scale, int4* s_pg, int4* s_pb, int4* s_ng, int4* s_nb, int at) const {
+    s_scale[at] = scale;
+    if (POST) {
+      s_pg[at] = widen(post_gamma);
+      s_pb[at] = post_beta;
+    }
+    if (PRE) {
+      s_ng[at] = widen(pre_gamma);
+      s_nb[at] = pre_beta;
+    }
+  }
+};
 
 // The requants' forms and the gate are decided per launch, not per element (a
 // test inside the unrolled words doubled the instructions: 47.6 per element
@@ -606,10 +629,13 @@ __global__ void __launch_bounds__(kResNormThreads<CPL>, 1) residual_norm_kernel(
   // every block has as many as any other
   const int64_t step = (int64_t)groups * gridDim.x;
   int64_t row = (int64_t)(threadIdx.x / LPR) * gridDim.x + blockIdx.x;
+  constexpr bool kFast = FORM != kFormAny;
+  const bool gated = FORM == kFormFastGate || (FORM == kFormAny && a.gate);
   // The tables may come from the kernel just before (a conditioning layer's output,
-  // say), as skip and branch do: they are brought towards the L2 before the wait, and
-  // read after it.  (Reading the tables after it alone took 12608 x 768 from 17.0 to 18.0 us;
-  // the first rows' prefetch wins that back.)
+  // say), as skip, branch and gate do: all are only brought towards the L2 before the
+  // wait, and read after it, the tables ahead of the first rows.  12608 x 768, both
+  // norms and a gate, cold: 17.2 us with the tables staged before the wait, 17.7
+  // after it and behind the rows, 16.8 ahead of them, 16.5 with the gate prefetched too.
   for (int i = threadIdx.x; i < cols / 32; i += blockDim.x) {
     prefetch_l2(a.scale + 32 * i);
     if (POST) {
@@ -621,18 +647,24 @@ __global__ void __launch_bounds__(kResNormThreads<CPL>, 1) residual_norm_kernel(
       if (i % 4 == 0) prefetch_l2(a.pre.gamma + 32 * i);
     }
   }
+  if (row < a.rows) {
+    // (a division of its own: sharing fetch's keeps its reciprocal live and spills, 17.1 us)
+    const int8_t* g = gated ? a.gate + row / a.gate_rows * cols : nullptr;
 #pragma unroll
-  for (int k = 0; k < CPL; ++k) {
-    const int ci = hl + LPR * k;
-    if (row < a.rows && ci < nchunk && hl % 2 == 0) {  // one lane per 32-byte sector
-      prefetch_l2(a.branch + row * cols + 16 * ci);
-      prefetch_l2(a.skip + row * cols + 16 * ci);
+    for (int k = 0; k < CPL; ++k) {
+      const int ci = hl + LPR * k;
+      if (ci < nchunk && hl % 2 == 0) {  // one lane per 32-byte sector
+        prefetch_l2(a.branch + row * cols + 16 * ci);
+        prefetch_l2(a.skip + row * cols + 16 * ci);
+        if (gated) prefetch_l2(g + 16 * ci);
+      }
     }
   }
-  pdl_wait();  // skip, branch and gate come from earlier kernels
+  pdl_wait();
   pdl_launch_dependents();
-  constexpr bool kFast = FORM != kFormAny;
-  const bool gated = FORM == kFormFastGate || (FORM == kFormAny && a.gate);
+  ResNormTables<POST, PRE> tables;
+  int ti = threadIdx.x;
+  if (ti < 4 * nchunk) tables.load(a, ti);
   int32_t plo = INT_MIN, phi = INT_MAX, nlo = INT_MIN, nhi = INT_MAX;
   if (POST && !kFast && !a.post.fast) out_bounds(a.post.out.b, a.post.out.c, plo, phi);
   if (PRE && !kFast && !a.pre.fast) out_bounds(a.pre.out.b, a.pre.out.c, nlo, nhi);
@@ -657,16 +689,10 @@ __global__ void __launch_bounds__(kResNormThreads<CPL>, 1) residual_norm_kernel(
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   fetch(row);
-  for (int i = threadIdx.x; i < cols / 4; i += blockDim.x) {  // behind the first rows' copies
-    stage_i32(s_scale, a.scale, i, nchunk);
-    if (POST) {
-      stage_gamma(s_pg, a.post.gamma, i, nchunk);
-      stage_i32(s_pb, a.post.beta, i, nchunk);
-    }
-    if (PRE) {
-      stage_gamma(s_ng, a.pre.gamma, i, nchunk);
-      stage_i32(s_nb, a.pre.beta, i, nchunk);
-    }
+  while (ti < 4 * nchunk) {
+    tables.store(s_scale, s_pg, s_pb, s_ng, s_nb, (ti & 3) * nchunk + (ti >> 2));
+    ti += blockDim.x;
+    if (ti < 4 * nchunk) tables.load(a, ti);
   }
   __syncthreads();
   for (int64_t row0 = blockIdx.x; row0 < a.rows; row0 += step, row += step) {  // the same trips for a warp's lanes
@@ -787,10 +813,12 @@ cudaError_t run_residual_norm(const DeviceCtx& dc, const ResNormArgs& a, cudaStr
   // few rows: smaller blocks, so that more SMs share them
   const int threads = a.rows * LPR <= (int64_t)256 * dc.num_sms ? 256 : kResNormThreads<CPL>;
   const size_t smem = (size_t)a.cols * 4 * (1 + (POST ? 2 : 0) + (PRE ? 2 : 0)) +
-                      (size_t)threads * 16 * CPL * (FORM == kFormFast ? 2 : 3);  // at most 136 KB
+                      (size_t)threads * 16 * CPL * (FORM == kFormFast ? 2 : 3);
+  constexpr int kMostSmem = 16 * LPR * CPL * 4 * 5 + kResNormThreads<CPL> * 16 * CPL * 3;  // the widest row of this form
+  static_assert(kMostSmem <= 138 * 1024, "shared memory of the widest row");
   static bool attr_done[64];  // per device; benign race: the attribute value is the same
   if (!attr_done[dc.device]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
     attr_done[dc.device] = true;
   }
