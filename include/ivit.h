@@ -25,6 +25,8 @@
  *     argument returns IVIT_ERR_INVALID_ARG (or IVIT_ERR_UNSUPPORTED for a
  *     shape outside the supported envelope) with nothing enqueued.  A failed
  *     launch returns IVIT_ERR_CUDA.
+ *   - Any tensor of a call, tables included, may be the output of an earlier
+ *     call or kernel on the same stream: none is read before that has ended.
  *   - Kernels never wait without bound: a wait that exceeds its budget (one
  *     second) records IVIT_ERR_TIMEOUT in a per-device status word, which
  *     ivit_stream_status() reads.
@@ -226,14 +228,18 @@ ivit_status ivit_layernorm_ptf(const int8_t *x, int64_t rows, int32_t cols, cons
  * tensors, dyadic requant with floor shifts, 32-bit accumulators).
  * ------------------------------------------------------------------------- */
 
-/* n low-rank adapters of one linear layer [N x K], all of rank R (a multiple
- * of 16, at most 128; a narrower adapter has zero rows of A).
+/* n >= 1 low-rank adapters of one linear layer [N x K], all of rank R (a
+ * multiple of 16, at most 128; a narrower adapter has zero rows of A).
  *   A   [n x R x K] int8, down projections
  *   b_t [n x R] int32 in [0, 2^31), c_t [n x R] int8 in [0, 31]: requant of
  *       t = X A^T to int8, b_t / 2^c_t ~ S_x S_A / S_t
  *   B   [n x N x R] int8, up projections, each entry at the scale
  *       S_x S_w[j] / S_t[r], so that t B^T joins the layer's accumulator as
- *       it is (|t B^T| <= 2^14 R accumulator units).                         */
+ *       it is (|t B^T| <= 2^14 R accumulator units).  B has no multiplier of
+ *       its own: |t B| is the rank entry's contribution in accumulator units
+ *       (S_x S_w[j]), and S_t[r] only divides it between the two.  An entry that
+ *       contributes at most u units leaves t and B about u levels between them:
+ *       2^14 fills both, 2^8 leaves 16 each, more than 2^14 saturates.        */
 typedef struct {
   int32_t n, R;
   const int8_t *A;
@@ -309,8 +315,10 @@ ivit_status ivit_residual_norm(const int8_t *skip, const int8_t *branch, int64_t
  * qkv [B*N x 3*D] int8, D = 128 * H: columns [0, D) are Q (Q^1 of head h at
  * 128 h, Q^2 at 128 h + 64), [D, 2D) K likewise, [2D, 3D) V (head h at 128 h).
  * lam [H] int32 (device), clamped to [0, 2^M].  ctx [B*N x D] int8.
- * Constraints: B, N >= 0, H >= 1; N <= 640; 2 <= k_s <= 8; I0 >= 1;
- * k_out - 1 <= M <= 30; 1 <= k_out <= 8.                                    */
+ * A lambda_h below 0 or above 1 has no form here: the clamp makes it 0 or 1 and
+ * is not reported, so a caller who may have one looks before the call.
+ * Constraints: B, N >= 0, H >= 1; 2 <= k_s <= 8; I0 >= 1; k_out - 1 <= M <= 30;
+ * 1 <= k_out <= 8.  N <= 640 and H <= 2048, else IVIT_ERR_UNSUPPORTED.        */
 ivit_status ivit_attention_diff(const int8_t *qkv, int32_t B, int32_t N, int32_t H, ivit_dyadic logit, int32_t k_s,
                                 int32_t I0, int32_t M, int32_t k_out, const int32_t *lam, ivit_dyadic out,
                                 int8_t *ctx, ivit_stream_t stream);

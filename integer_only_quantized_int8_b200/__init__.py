@@ -402,7 +402,9 @@ def ivit_linear_lora(X, W, bias, b, c, adapters, idx, rows: int, Y, workspace, o
                      stream=None, rounding: int = 0):
     """ivit_linear_requant with a low-rank adapter per request: rows [q * rows, (q + 1) * rows) of X take adapter
     idx[q] of ``adapters`` = (A [n,R,K] int8, b_t [n,R] int32, c_t [n,R] int8, B [n,N,R] int8), or none where idx[q]
-    is outside [0, n)."""
+    is outside [0, n).  t = sat_8((b_t (X A^T)) >> c_t) and t B^T joins the layer's accumulator as it is: B lies at the
+    scale S_x S_w[j] / S_t[r] and has no multiplier of its own, so a rank entry that contributes at most u accumulator
+    units leaves t and B about u levels between them (2^14 fills both, 2^8 leaves 16 each)."""
     st = (_calls or _native()).linear_lora(X, W, bias, b, c, adapters, idx, rows, Y, workspace, out_bits, skip,
                                              _triple(res), stream, rounding)
     if st:
@@ -425,7 +427,8 @@ def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, g
     """The end of a residual branch in one pass: y = sat_8((b_skip skip + scale_j u) >> c) with u the branch, after
     its I-LayerNorm ``post`` and times its request's row of ``gate``, and z = I-LayerNorm ``pre`` of y.  skip, branch,
     y, z [rows, cols] int8; post and pre (gamma, beta, F, M_ln, out) or None; gate [ceil(rows / gate_rows), cols] int8
-    or None; scale [cols] int32.  y and z may each be skip or branch itself.  Returns (y, z)."""
+    or None; scale [cols] int32.  y and z may each be skip or branch itself; any other overlap of theirs with a tensor
+    of the call is refused.  Returns (y, z)."""
     st = (_calls or _native()).residual_norm(skip, branch, scale, b_skip, c, y, post, gate, gate_rows, pre, z, stream)
     if st:
         _check("ivit_residual_norm", st)
@@ -435,7 +438,8 @@ def ivit_residual_norm(skip, branch, scale, b_skip: int, c: int, y, post=None, g
 def ivit_attention_diff(qkv, B: int, N: int, H: int, logit, k_s: int, I0: int, M: int, k_out: int, lam, out, ctx,
                         stream=None):
     """ctx [B*N, 128*H] from qkv [B*N, 3*128*H]: each head attends with the difference of two Shiftmax maps, the second
-    weighted by lam[h] / 2^M (lam [H] int32)."""
+    weighted by lam[h] / 2^M (lam [H] int32).  lam is clamped to [0, 2^M] without a report: a weight below 0 or above 1
+    has no form here."""
     st = (_calls or _native()).attention_diff(qkv, B, N, H, logit, k_s, I0, M, k_out, lam, out, ctx, stream)
     if st:
         _check("ivit_attention_diff", st)

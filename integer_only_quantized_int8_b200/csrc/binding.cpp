@@ -1,11 +1,12 @@
 // binding.cpp -- the Python calls of the serving operators, marshalled natively.
 //
 // Their small calls run for 3 to 10 us on the GPU, less than a dozen tensors took
-// to check and pass through ctypes (9.8 to 13.7 us a call; 3.3 to 6.4 here).  Same
-// checks, same errors as the ctypes wrappers in __init__.py: every tensor must
+// to check and pass through ctypes (9.8 to 13.7 us a call; 3.3 to 6.4 here).  The
+// checks and errors are those of the ctypes wrappers in __init__.py: every tensor must
 // be a contiguous CUDA tensor of its type on the current device and hold what
 // the library reads or writes; a non-OK status comes back as a number for the
-// caller to raise.
+// caller to raise.  Sizes and plain arguments come first, so that a call which
+// they spoil is refused whatever device its tensors are on.
 #include <Python.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>

@@ -34,11 +34,13 @@
 // (w, w + 4 of each group) split a row's keys; partial maxima and sums meet in
 // shared memory.
 //
-// What bounds it: about 8 integer instructions a score, 10.6 us of the fullest
-// pipe for 64 x 197 tokens in 6 head pairs, against 36.4 us measured (577 tokens,
-// batch 16: 67.8; 197 tokens, 3 pairs, one image: 9.8).  The passes are dependent
-// chains of four warps per scheduler (0.53 instructions a cycle); more warps do
-// not fit the registers and the counters show no pipe above 42 %.
+// What bounds it: 64 x 197 tokens in 6 head pairs are 19.2 M warp instructions, 15.9
+// per 32 scores (rows and keys padded to 224), hence 16.5 us of issue slots and 17 of
+// the ALU pipe, against 37.3 us measured from HBM (577 tokens, batch 16: 67.9; 197
+// tokens, 3 pairs, one image: 9.8).  The rest is latency: the passes are dependent
+// chains (TMEM load, table address, table load, byte pack) of four softmax warps per
+// scheduler with one TMEM load in flight each, the slots are half used and waits for
+// loads are the largest stall; no pipe is above 42 %.
 //
 // Keys past the last one are masked where they lie: out of the maximum and the
 // sum, and to P = 0.  Whatever their logit bytes hold, their table addresses stay

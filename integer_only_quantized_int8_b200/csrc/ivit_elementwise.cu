@@ -168,9 +168,9 @@ __device__ __forceinline__ int32_t sext_byte(uint32_t w, int i) {
 // kernel of the same library call vouches for them (it has waited for whatever was
 // enqueued before the call); else they may come from the kernel just before, a
 // conditioning layer's output say, and are staged after the wait, behind the row's
-// own loads.  Measured, us, early / late: back to back 197 x 192 1.83 / 2.03,
-// 12608 x 384 6.0 / 6.0, 6304 x 1024 6.4 / 7.6, 12608 x 768 10.1 / 7.9; a DeiT-S block
-// at batch 64, both norms early 76.2, the first one late 76.5, both late 77.8.  Sums of x and x^2 come
+// own loads.  Measured, us, early / late: back to back 197 x 192 1.82 / 1.95,
+// 12608 x 384 6.0 / 6.0, 6304 x 1024 6.4 / 7.6, 12608 x 768 10.2 / 8.0; a DeiT-S block
+// at batch 64, both norms early 76.5, the first one late 76.9, both late 77.8.  Sums of x and x^2 come
 // from dp4a; the mean and variance divisions and 2^M / sigma use an exact
 // fp32 reciprocal quotient with one integer correction (udiv_fast); the root
 // is isqrt_newton10; then the per-element normalisation, affine and dyadic
@@ -489,8 +489,10 @@ __global__ void __launch_bounds__(kPtfThreads)
 // bytes of the separate operators.  kLnLanes lanes share a row as in
 // layernorm_staged_kernel; the per-channel tables are staged in shared memory
 // by each block, which then walks rows.  12608 x 768 with both norms and a gate
-// takes 15.4 us from L2 (16.1 from HBM, whose bandwidth would allow 6): 31.6 warp
-// instructions an element, 8.6 us of issue slots.
+// takes 16.3 us from HBM, whose bandwidth would allow 6: 11.7 M warp instructions,
+// 38.6 per 32 elements, are 10.0 us of issue slots, and the FMA pipe's heavy half (two
+// 64-bit products and two mul.hi an element) is busy for 10.9 of the 21.2 us that the
+// launch takes with cold caches.
 // ---------------------------------------------------------------------------
 struct NormArgs {
   const int8_t* gamma;
@@ -591,9 +593,8 @@ struct ResNormTables {
   }
 };
 
-// The requants' forms and the gate are decided per launch, not per element (a
-// test inside the unrolled words doubled the instructions: 47.6 per element
-// and 21.8 us for 12608 x 768): kFormFast / kFormFastGate when both norms'
+// The requants' forms and the gate are decided per launch, not per element (with
+// a test inside the unrolled words 12608 x 768 took 21.8 us, 16.2 without): kFormFast / kFormFastGate when both norms'
 // requants are one mul.hi and the residual sum's shift fits int32, without and
 // with a gate; kFormAny tests as it goes.
 enum ResNormForm : int { kFormAny = 0, kFormFast = 1, kFormFastGate = 2 };

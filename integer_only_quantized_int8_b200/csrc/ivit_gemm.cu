@@ -1736,6 +1736,11 @@ int pick_bn_own(int64_t M, int N, int num_sms) {
 // W^O 8.9 / 7.8, fc1 16.0 / 14.0; ViT-B fc1 30.1 / 27.5; but ViT-B QKV
 // 18.8 / 20.3, W^O 13.0 / 13.5, fc2 25.9 / 29.9 and every ViT-L layer were
 // slower (tiles of at most 160 tokens take an extra round of tiles there).
+// With adapters the rule was looked at again (16 per 64 images, from HBM, us, shared
+// with at most 192 tokens / own): DeiT-S QKV R = 16 17.0 / 16.5, R = 64 23.5 / 23.2, W^O
+// 14.0 / 13.1, fc1 23.0 / 21.9; ViT-B fc1 R = 64 53.6 / 52.3, but R = 16 41.0 / 44.1: own
+// tiles of 160 and 144 tokens have a ring of three beside the adapters' stage, and
+// so one MMA issuer.
 template <int EPI>
 bool use_own_tiles(int K) {
   return K <= 512 || (EPI == kEpiGelu && K <= 768);
