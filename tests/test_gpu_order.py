@@ -155,3 +155,57 @@ def test_block_tables_of_the_call_before(place):
     assert (want[0] != want[1]).any()
     for k in range(CALLS):
         np.testing.assert_array_equal(outs[k][0].cpu().numpy(), want[k & 1])
+
+
+GELU = (27, 30, 8, (1476395008, 27))
+# one kernel; a down projection, then k-slices of the shared-tile and own-tile GEMM; then dp4a of short and long ranks
+LAYERS = [(4, 50, 256, 512, 16, 4), (24, 33, 784, 528, 64, 8), (24, 65, 256, 1040, 16, 3), (90, 1, 256, 528, 16, 40),
+          (60, 1, 272, 400, 64, 20)]
+
+
+@pytest.mark.parametrize("layer,form", list(zip(LAYERS, [(1, 64), (2, 128), (2, 128), (3, 16), (4, 16)])))
+@pytest.mark.parametrize("place", ["first", "last"])
+@pytest.mark.parametrize("gelu", [False, True])
+def test_adapter_tables_of_the_call_before(layer, form, place, gelu):
+    """Everything that a layer with adapters reads, its own weights and input among it."""
+    from test_gpu_serving import LoraCase
+    req, rows, K, N, R, n = layer
+    assert ivit.ivit_selftest_lora_form(req * rows, K, N, n, R, rows, gelu)[:2] == form
+    qs = [LoraCase(req, rows, K, N, R, n, seed=i) for i in (1, 2)]
+    shapes = {"X": (req * rows, K), "W": (N, K), "A": (n, R, K), "b_t": (n, R), "c_t": (n, R), "B": (n, N, R)}
+    sets = [dict(X=q.X, W=q.W, bias=q.bias, b=q.b, c=q.c, A=q.adapters[0], b_t=q.adapters[1], c_t=q.adapters[2],
+                 B=q.adapters[3], idx=q.idx) for q in qs]
+    t = Tables([{k: np.ascontiguousarray(v).reshape(-1) for k, v in s.items()} for s in sets], place)
+    v = {k: t.view(k).view(shapes[k]) if k in shapes else t.view(k) for k in sets[0]}
+    outs = [(torch.zeros(req * rows, N, dtype=torch.int8, device="cuda"),) for _ in range(CALLS)]
+    ws = torch.zeros(ivit.ivit_linear_lora_workspace_bytes(req * rows, R), dtype=torch.uint8, device="cuda")
+    args = (v["X"], v["W"], v["bias"], v["b"], v["c"], (v["A"], v["b_t"], v["c_t"], v["B"]), v["idx"], rows)
+
+    def call(k):
+        if gelu:
+            ivit.ivit_linear_lora_shiftgelu(*args, *GELU, outs[k][0], ws)
+        else:
+            ivit.ivit_linear_lora(*args, outs[k][0], ws, skip=outs[0][0], res=(0, 1 << 20, 20))
+
+    run(t, call, outs, False)
+    want = [serving.linear_lora(*q.host(), gelu=GELU if gelu else None) for q in qs]
+    assert (want[0] != want[1]).any()
+    for k in range(CALLS):
+        np.testing.assert_array_equal(outs[k][0].cpu().numpy(), want[k & 1])
+
+
+@pytest.mark.parametrize("N", [65, 300])
+@pytest.mark.parametrize("place", ["first", "last"])
+def test_attention_diff_inputs_of_the_call_before(N, place):
+    B, H, args = 2, 2, ((1 << 20, 28), 8, 20, 30, 8)
+    r = np.random.default_rng(N)
+    sets = [{"qkv": np.clip(np.round(r.standard_normal(B * N * 384 * H) * 30), -128, 127).astype(np.int8),
+             "lam": r.integers(0, (1 << 30) + 1, H).astype(np.int32)} for _ in range(2)]
+    t = Tables(sets, place)
+    qkv, lam = t.view("qkv").view(B * N, 384 * H), t.view("lam")
+    outs = [(torch.zeros(B * N, 128 * H, dtype=torch.int8, device="cuda"),) for _ in range(CALLS)]
+    run(t, lambda k: ivit.ivit_attention_diff(qkv, B, N, H, *args, lam, (1 << 20, 25), outs[k][0]), outs, False)
+    want = [serving.attention_diff(s["qkv"].reshape(B * N, 384 * H), B, N, H, *args, s["lam"], (1 << 20, 25)) for s in sets]
+    assert (want[0] != want[1]).any()
+    for k in range(CALLS):
+        np.testing.assert_array_equal(outs[k][0].cpu().numpy(), want[k & 1])
