@@ -169,11 +169,12 @@ __device__ __forceinline__ int32_t sext_byte(uint32_t w, int i) {
 // enqueued before the call); else they may come from the kernel just before, a
 // conditioning layer's output say, and are staged after the wait, behind the row's
 // own loads.  Measured, us, early / late: back to back 197 x 192 1.82 / 1.95,
-// 12608 x 384 6.0 / 6.0, 6304 x 1024 6.4 / 7.6, 12608 x 768 10.2 / 8.0; a DeiT-S block
-// at batch 64, both norms early 76.5, the first one late 76.9, both late 77.8.  Sums of x and x^2 come
-// from dp4a; the mean and variance divisions and 2^M / sigma use an exact
-// fp32 reciprocal quotient with one integer correction (udiv_fast); the root
-// is isqrt_newton10; then the per-element normalisation, affine and dyadic
+// 12608 x 384 6.0 / 6.0, 6304 x 1024 6.4 / 7.6, 12608 x 768 10.2 / 8.0; a block with
+// both norms early / with its first norm late: DeiT-S at batch 64 76.9 / 77.4 (both
+// late: 1.1 more than both early), ViT-B at 64 152.0 / 150.1, ViT-L at 32 124.6 / 123.1.
+// Sums of x and x^2 come from dp4a; the mean and variance divisions and 2^M / sigma
+// use an exact fp32 reciprocal quotient with one integer correction (udiv_fast); the
+// root is isqrt_newton10; then the per-element normalisation, affine and dyadic
 // requant.  CLAMP = false when the host has shown that (b acc) >> c fits
 // int32 for every reachable acc; FASTQ: the requant is one mul.hi.
 constexpr int kLnLanes = 16;  // a half-warp per row
